@@ -1,0 +1,375 @@
+"""The coded cache, the attention over it and the eviction on the GPU, against
+their plain forms in 64 bits (tests/cache_helpers.py)."""
+import numpy as np
+import pytest
+
+import cache_helpers as ch
+from gpu_helpers import ATTN_TOL, need_gpu
+
+pytestmark = pytest.mark.gpu
+
+LENGTHS = [0, 1, 2, 3, 4, 5, 15, 16, 17, 63, 64, 65, 67, 127, 128, 131, 509, 2048, 2051, 4096, 4099, 4101, 9001]
+HEADS = [(1, 1, 64), (2, 2, 64), (8, 2, 64), (16, 2, 128), (16, 1, 128), (10, 2, 128), (12, 1, 64), (9, 1, 128), (24, 8, 128)]
+
+
+def _ok(t):
+    from top_group_sparse_gb300 import qsa
+    st, flags = qsa.qsa_check_errors(t["ws"])
+    assert st == 0, f"device error word {flags:#x}"
+
+
+def _flags(t):
+    from top_group_sparse_gb300 import qsa
+    return qsa.qsa_check_errors(t["ws"])[1]
+
+
+def _attend(t, ids=None, n_ids=None, weights=False, stream=None):
+    from top_group_sparse_gb300 import qsa
+    qsa.qsa_attend_coded(t["dims"], t["inputs"], t["cache"], ids, n_ids, t["out"], t["ws"],
+                         weights=t["weights"] if weights else None,
+                         weight_offset=t["weight_offset"] if weights else None, stream=stream)
+    return t["out"]
+
+
+def _close(h, got, ref, tol, standard=True):
+    got = got.cpu().numpy().astype(np.float64)
+    assert np.isfinite(got).all()
+    for b in range(h.B):
+        err = np.abs(got[b] - ref[b]).max()
+        assert err <= tol[b], f"query {b} (T {h.visible[b]}): {err:.3e} > {tol[b]:.3e}"
+        if standard:  # the library's bar for values drawn from N(0, 1)
+            assert err <= ATTN_TOL * 6, f"query {b}"
+
+
+# ---- coding ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("kv,d", [(1, 64), (3, 64), (2, 128), (8, 128)])
+def test_codes_and_scales_equal_the_definition(fmt, kv, d):
+    need_gpu()
+    h = ch.History([0, 3, 4, 7, 64, 1029, 517], q_heads=kv, kv_heads=kv, head_dim=d, fmt=fmt, seed=3)
+    h.k *= np.exp(3 * np.random.RandomState(1).randn(len(h.k), 1, 1)).astype(np.float32)
+    h.k_cache[h.slot_map] = h.k
+    t = ch.device(h)
+    t["codes"].fill_(0x5a)
+    t["scales"].fill_(-3.0)
+    ch.fill_cache(h, t)
+    _ok(t)
+    K, V = ch.unpack(t["codes"].cpu().numpy(), d, fmt)
+    s = t["scales"].cpu().numpy()
+    done = np.zeros(h.num_blocks, bool)
+    for b, T in enumerate(h.visible):
+        n = int(T) // 4
+        blk = h.block_map[h.group_offset[b]:h.group_offset[b] + n]
+        done[blk] = True
+        for src, got, i in ((h.k, K, 0), (h.v, V, 1)):
+            x = src[h.token_offset[b]:h.token_offset[b] + 4 * n].reshape(n, 4, kv, d).transpose(0, 2, 1, 3)
+            c, sc = ch.encode(x, fmt)
+            assert np.array_equal(s[blk, :, i], sc)
+            assert np.array_equal(got[blk], c)
+    # blocks of no group are left as they were
+    assert (t["codes"].cpu().numpy()[~done] == 0x5a).all() and (s[~done] == -3.0).all()
+
+
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_coding_of_extreme_groups(fmt, d):
+    """Zero, tiny, subnormal, huge, infinite and NaN groups, each beside an ordinary one."""
+    need_gpu()
+    vals = [0.0, 1e-45, 1e-38, 5e-36, 6e-36, 1e-30, 3.0e38, np.inf, -np.inf, np.nan, 1.0]
+    h = ch.History([4 * len(vals)], q_heads=2, kv_heads=2, head_dim=d, fmt=fmt, seed=5)
+    for i, v in enumerate(vals):
+        if v == 0 or abs(v) < 1e-20:
+            h.k[4 * i:4 * i + 4] = (np.random.RandomState(i).rand(4, 2, d) * v).astype(np.float32)
+        h.k[4 * i + i % 4, 0, (7 * i) % d] = v     # head 0 only
+        h.v[4 * i + 3, 1, (5 * i) % d] = v
+    h.k_cache[h.slot_map], h.v_cache[h.slot_map] = h.k, h.v
+    t = ch.device(h)
+    ch.fill_cache(h, t)
+    _ok(t)
+    K, V = ch.unpack(t["codes"].cpu().numpy(), d, fmt)
+    s = t["scales"].cpu().numpy()
+    blk = h.block_map[:len(vals)]
+    for src, got, j in ((h.k, K, 0), (h.v, V, 1)):
+        x = src.reshape(len(vals), 4, 2, d).transpose(0, 2, 1, 3)
+        c, sc = ch.encode(x, fmt)
+        assert np.array_equal(s[blk, :, j], sc, equal_nan=True)
+        assert np.array_equal(got[blk], c)
+
+
+def test_coding_flags_and_skips_what_is_out_of_range():
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    h = ch.History([64, 64, 64], q_heads=2, kv_heads=2, head_dim=64, fmt=ch.E4M3, seed=6)
+    t = ch.device(h)
+    for lo, hi, most in (([-1, 0, 0], [1, 0, 0], 1), ([0, 5, 0], [0, 4, 0], 1), ([0, 0, 16], [0, 0, 17], 1), ([0, 0, 0], [0, 2, 0], 1)):
+        t["codes"].fill_(9)
+        qsa.qsa_code_groups(t["dims"], t["inputs"], t["cache"], torch.tensor(lo, dtype=torch.int32, device="cuda"),
+                            torch.tensor(hi, dtype=torch.int32, device="cuda"), most, t["ws"])
+        assert _flags(t) == qsa.QSA_DEVERR_VISIBLE_RANGE
+        assert (t["codes"] == 9).all()
+    # a block outside the cache is skipped, a slot outside it codes zeros; the others are coded
+    bm, sl = t["block_map"].clone(), t["slot_map"].clone()
+    t["block_map"][3] = h.num_blocks
+    t["block_map"][4] = -1
+    t["slot_map"][8] = h.num_slots
+    t["slot_map"][9] = -7
+    t["codes"].zero_()
+    ch.fill_cache(h, t)
+    assert _flags(t) == qsa.QSA_DEVERR_SLOT_RANGE
+    K, _ = ch.unpack(t["codes"].cpu().numpy(), 64, h.fmt)
+    for g in range(48):
+        if g in (3, 4):
+            assert (K[int(bm[g])] == 0).all()
+            continue
+        x = h.k[4 * g:4 * g + 4].copy()
+        if g == 2:
+            x[:2] = 0
+        assert np.array_equal(K[int(bm[g])], ch.encode(x.transpose(1, 0, 2), h.fmt)[0]), g
+    t["block_map"].copy_(bm)
+    t["slot_map"].copy_(sl)
+    # the same block named by two queries of one history
+    h = ch.History([40, 40], q_heads=2, kv_heads=2, head_dim=64, fmt=ch.E4M3, seed=7, shared=True)
+    t = ch.device(h)
+    both = torch.tensor([10, 10], dtype=torch.int32, device="cuda")
+    qsa.qsa_code_groups(t["dims"], t["inputs"], t["cache"], both - 10, both, 10, t["ws"])
+    _ok(t)
+    K, _ = ch.unpack(t["codes"].cpu().numpy(), 64, h.fmt)
+    assert np.array_equal(K[h.block_map[:10]], ch.encode(h.k.reshape(10, 4, 2, 64).transpose(0, 2, 1, 3), h.fmt)[0])
+
+
+# ---- attention ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("q_heads,kv,d", HEADS)
+def test_attention_over_whole_histories(fmt, q_heads, kv, d):
+    need_gpu()
+    h = ch.History(LENGTHS, q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=11)
+    t = ch.device(h, whole=True, weights=True)
+    ch.fill_cache(h, t)
+    ref, share, tol, rel = ch.attention(h)
+    _close(h, _attend(t), ref, tol)
+    _ok(t)
+    first = t["out"].clone()
+    # with weights: the same output, and the shares added
+    _attend(t, weights=True)
+    _ok(t)
+    assert (t["out"] == first).all()
+    w, wt = ch.add_weights(h, share, rel)
+    got = t["weights"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()
+    assert abs((got - h.weights0).sum() - q_heads * np.count_nonzero(h.visible)) < 1e-3 * q_heads
+
+
+@pytest.mark.parametrize("budget", [512, 32, 5, 1])
+@pytest.mark.parametrize("fmt,q_heads,kv,d", [(ch.E4M3, 16, 2, 128), (ch.INT8, 8, 2, 64), (ch.INT8, 16, 1, 128), (ch.E4M3, 3, 3, 64)])
+def test_attention_over_selected_rows(budget, fmt, q_heads, kv, d):
+    need_gpu()
+    h = ch.History([0, 1, 3, 4, 6, 70, 128, 131, 2051, 9002, 4097], q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=12)
+    rows = ch.some_rows(h, budget, 13)
+    t = ch.device(h, budget=budget, weights=True)
+    ch.fill_cache(h, t)
+    ids, n = ch.rows_to_device(rows, budget)
+    ref, share, tol, rel = ch.attention(h, rows)
+    _close(h, _attend(t, ids, n), ref, tol)
+    first = t["out"].clone()
+    _attend(t, ids, n, weights=True)
+    _ok(t)
+    assert (t["out"] == first).all()
+    w, wt = ch.add_weights(h, share, rel)
+    got = t["weights"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_weights_of_a_shared_history_are_added_in_batch_order(whole):
+    torch = need_gpu()
+    vis = [997 + i for i in range(37)]
+    h = ch.History(vis, q_heads=8, kv_heads=2, head_dim=64, fmt=ch.INT8, seed=14, shared=True)
+    t = ch.device(h, budget=64, whole=whole, weights=True)
+    ch.fill_cache(h, t)
+    rows = None if whole else ch.some_rows(h, 64, 15)
+    ids, n = (None, None) if whole else ch.rows_to_device(rows, 64)
+    ref, share, tol, rel = ch.attention(h, rows)
+    _close(h, _attend(t, ids, n, weights=True), ref, tol)
+    _ok(t)
+    w, wt = ch.add_weights(h, share, rel)
+    got = t["weights"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()
+    again = t["weights"].clone()
+    for _ in range(3):
+        t["weights"].copy_(torch.from_numpy(h.weights0))
+        _attend(t, ids, n, weights=True)
+        assert torch.equal(t["weights"], again)
+
+
+def test_an_output_does_not_depend_on_the_batch_or_the_workspace():
+    """Each query alone, in a workspace made for its own length, gives the bits it
+    gives in the batch, call after call."""
+    torch = need_gpu()
+    h = ch.History([4101, 77, 9001, 0, 640], q_heads=16, kv_heads=2, head_dim=128, fmt=ch.E4M3, seed=16)
+    t = ch.device(h, whole=True)
+    ch.fill_cache(h, t)
+    out = _attend(t).clone()
+    assert torch.equal(_attend(t), out)
+    from top_group_sparse_gb300 import qsa
+    for b in range(h.B):
+        dims = qsa.make_dims(1, 8, 64, 16, 2, 128, max_visible=int(h.visible[b]) + 1000 * b, scale=h.scale)
+        ws = torch.zeros(qsa.qsa_coded_workspace_size(dims, True), dtype=torch.uint8, device="cuda")
+        inp = qsa.QsaInputs(visible=t["visible"][b:].data_ptr(), q=t["q"][b:].data_ptr(), k_cache=t["k_cache"].data_ptr(),
+                            v_cache=t["v_cache"].data_ptr(), num_slots=h.num_slots, slot_map=t["slot_map"].data_ptr(),
+                            slot_offset=t["token_offset"][b:].data_ptr())
+        cache = qsa.QsaCodedCache.of(t["codes"], t["scales"], t["block_map"], t["group_offset"][b:], h.fmt)
+        one = torch.full((1, 16, 128), float("nan"), device="cuda")
+        qsa.qsa_attend_coded(dims, inp, cache, None, None, one, ws)
+        assert torch.equal(one[0], out[b]), b
+
+
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+def test_wide_ranges_of_scales_and_scores(fmt):
+    """Scores spread over hundreds (one token takes all the weight), queries and
+    groups whose sizes differ by 2^40, zero queries."""
+    need_gpu()
+    h = ch.History([2000, 2000, 333, 1200], q_heads=8, kv_heads=2, head_dim=128, fmt=fmt, seed=17)
+    r = np.random.RandomState(18)
+    h.q[0] *= 60
+    h.q[2] = 0
+    h.q[3] *= 2.0 ** -20
+    for x in (h.k, h.v):
+        x[h.token_offset[3]:] *= 2.0 ** 20
+    h.v[:2000] *= np.repeat(2.0 ** r.randint(-20, 20, 500), 4)[:, None, None].astype(np.float32)
+    h.k_cache[h.slot_map], h.v_cache[h.slot_map] = h.k, h.v
+    t = ch.device(h, whole=True)
+    ch.fill_cache(h, t)
+    ref, _, tol, _ = ch.attention(h)
+    _close(h, _attend(t), ref, tol, standard=False)
+    _ok(t)
+
+
+def test_groups_that_are_not_finite_reach_only_what_attends_to_them():
+    need_gpu()
+    h = ch.History([400, 400], q_heads=4, kv_heads=2, head_dim=64, fmt=ch.INT8, seed=19)
+    h.k[40, 1, 5] = np.nan           # query 0, group 10, head 1
+    h.v[400 + 44, 0, 3] = np.inf     # query 1, group 11, head 0
+    h.k_cache[h.slot_map], h.v_cache[h.slot_map] = h.k, h.v
+    t = ch.device(h, whole=True)
+    ch.fill_cache(h, t)
+    out = _attend(t).cpu().numpy()
+    assert np.isnan(out[0, 2:]).all() and np.isfinite(out[0, :2]).all()
+    assert np.isnan(out[1, :2]).all() and np.isfinite(out[1, 2:]).all()
+    # rows without those groups
+    rows = [np.r_[0:40, 44:400], np.r_[0:44, 48:400]]
+    ids, n = ch.rows_to_device(rows, 512)
+    out = _attend(t, ids, n).cpu().numpy()
+    assert np.isfinite(out).all()
+    _ok(t)
+    # what the f32 cache holds in slots that no tail names is not read
+    h = ch.History([402, 7], q_heads=4, kv_heads=2, head_dim=64, fmt=ch.INT8, seed=20)
+    t = ch.device(h, whole=True)
+    ch.fill_cache(h, t)
+    tails = np.concatenate([h.slot_map[400:402], h.slot_map[402 + 4:402 + 7]])
+    other = np.setdiff1d(np.arange(h.num_slots), tails)
+    t["k_cache"][other] = float("nan")
+    t["v_cache"][other] = float("inf")
+    ref, _, tol, _ = ch.attention(h)
+    _close(h, _attend(t), ref, tol)
+
+
+def test_attention_flags_what_is_out_of_range():
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    h = ch.History([100, 203, 64, 40], q_heads=4, kv_heads=2, head_dim=64, fmt=ch.E4M3, seed=21)
+    t = ch.device(h, budget=32, whole=True, weights=True)
+    ch.fill_cache(h, t)
+    good = _attend(t).clone()
+    vis = t["visible"].clone()
+    for bad in (-1, 204):
+        t["visible"].copy_(vis)
+        t["visible"][1] = bad
+        before = t["weights"].clone()
+        _attend(t, weights=True)
+        assert _flags(t) == qsa.QSA_DEVERR_VISIBLE_RANGE
+        assert (t["out"][1] == 0).all() and torch.equal(t["out"][[0, 2, 3]], good[[0, 2, 3]])
+        lo = int(h.weight_offset[1])
+        assert torch.equal(t["weights"][lo:lo + 51], before[lo:lo + 51])  # adds no weight
+        assert (t["weights"][:25] > before[:25]).all()
+    t["visible"].copy_(vis)
+    # blocks and slots outside their caches: zero rows
+    bm = t["block_map"].clone()
+    t["block_map"][int(h.group_offset[2]) + 5] = h.num_blocks
+    K, V = h.coded()
+    K[h.group_offset[2] + 5] = 0
+    V[h.group_offset[2] + 5] = 0
+    sl = t["slot_map"].clone()
+    t["slot_map"][int(h.token_offset[1]) + 202] = -1
+    kk, vv = h.k.copy(), h.v.copy()
+    h.k[h.token_offset[1] + 202] = 0
+    h.v[h.token_offset[1] + 202] = 0
+    ref, _, tol, _ = ch.attention(h, coded=(K, V))
+    _close(h, _attend(t), ref, tol)
+    assert _flags(t) == qsa.QSA_DEVERR_SLOT_RANGE
+    h.k, h.v = kk, vv
+    t["block_map"].copy_(bm)
+    t["slot_map"].copy_(sl)
+    # rows: counts out of range give zeros; a malformed group is a zero row, and the query adds no weight
+    base = ch.some_rows(h, 20, 22)
+    for b, change in enumerate(("neg", "long", "odd", "order")):
+        rows = [r.copy() for r in base]
+        ids, n = ch.rows_to_device(rows, 32)
+        if change == "neg":
+            n[b] = -1
+        elif change == "long":
+            n[b] = 4 * 32 + 4
+        elif change == "odd":
+            ids[b, 9] += 1
+        else:
+            ids[b, :8] = torch.cat([ids[b, 4:8].clone(), ids[b, :4].clone()])
+        before = t["weights"].clone()
+        _attend(t, ids, n, weights=True)
+        assert _flags(t) == qsa.QSA_DEVERR_ROW_RANGE, change
+        lo, hi = int(h.weight_offset[b]), int(h.weight_offset[b]) + -(-int(h.visible[b]) // 4)
+        assert torch.equal(t["weights"][lo:hi], before[lo:hi]), change
+        others = [o for o in range(4) if o != b]
+        for o in others:
+            lo, hi = int(h.weight_offset[o]), int(h.weight_offset[o]) + -(-int(h.visible[o]) // 4)
+            assert not torch.equal(t["weights"][lo:hi], before[lo:hi])
+        if b < 2:
+            assert (t["out"][b] == 0).all()
+        if change == "order":  # the attention itself takes any order
+            ref, _, tol, _ = ch.attention(h, base)
+            _close(h, t["out"], ref, tol)
+
+
+def test_a_captured_call_replays_on_new_inputs_and_another_stream():
+    """Coding and attention with weights captured once, replayed on other rows of the
+    f32 cache, with eager calls on another workspace in between."""
+    torch = need_gpu()
+    h = ch.History([517, 66], q_heads=16, kv_heads=2, head_dim=128, fmt=ch.INT8, seed=23)
+    t = ch.device(h, whole=True, weights=True)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ch.fill_cache(h, t)
+        _attend(t, weights=True)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ch.fill_cache(h, t)
+        _attend(t, weights=True)
+    h2 = ch.History([517, 66], q_heads=16, kv_heads=2, head_dim=128, fmt=ch.INT8, seed=24)
+    h2.slot_map, h2.block_map = h.slot_map, h.block_map
+    h2.k_cache[h.slot_map], h2.v_cache[h.slot_map] = h2.k, h2.v
+    for hh in (h2, h):
+        t["k_cache"].copy_(torch.from_numpy(hh.k_cache))
+        t["v_cache"].copy_(torch.from_numpy(hh.v_cache))
+        t["q"].copy_(torch.from_numpy(hh.q))
+        t["weights"].copy_(torch.from_numpy(hh.weights0))
+        g.replay()
+        ref, share, tol, rel = ch.attention(hh)
+        _close(hh, t["out"], ref, tol)
+        w, wt = ch.add_weights(hh, share, rel)
+        assert (np.abs(t["weights"].cpu().numpy() - w) <= wt).all()
+        t2 = ch.device(h, whole=True)
+        ch.fill_cache(h, t2)
+        _attend(t2)
+        _ok(t2)
+    _ok(t)

@@ -8,6 +8,7 @@
 
 #include <cstring>
 
+#include "cache_internal.cuh"
 #include "qsa_internal.cuh"
 #include "qsa_selftest.h"
 
@@ -64,10 +65,6 @@ Layout make_layout(const qsa_dims *d)
     return L;
 }
 
-namespace {
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 int num_sms_of_current_device()
 {
     static int cache[64] = {};
@@ -81,6 +78,10 @@ int num_sms_of_current_device()
     }
     return cache[dev];
 }
+
+namespace {
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 qsa_status check_ws(const qsa_dims *d, void *ws, size_t ws_bytes)
 {
@@ -208,6 +209,17 @@ qsa_status check_shapes(const qsa_dims *d, bool score, bool attend)
 }
 
 }  // namespace
+
+qsa_status score_and_select(const qsa_dims *d, const qsa_inputs *in, const float *pooled, const int64_t *pool_offset,
+                            void *ws, const Layout &L, cudaStream_t s)
+{
+    float *scores = ws_at<float>(ws, L.off_scores);
+    const qsa_status st = do_score(d, in, scores, L.score_stride, ws, L, s, pooled, pool_offset);
+    if (st != QSA_OK) return st;
+    return do_select(d, in->visible, scores, L.score_stride, ws_at<int32_t>(ws, L.off_ids),
+                     ws_at<int32_t>(ws, L.off_nids), ws, L, s, true, true, pooled == nullptr);
+}
+
 }  // namespace qsa
 
 using namespace qsa;

@@ -1,0 +1,124 @@
+// cache_internal.cuh -- internal declarations of the coded cache, the attention
+// over it and the eviction (include/qsa_cache.h).
+#pragma once
+
+#include "qsa_cache.h"
+#include "qsa_internal.cuh"
+
+namespace qsa {
+
+// ---- how a row is cut ---------------------------------------------------------
+// A row of n complete groups is cut into runs of run_groups(n) consecutive
+// groups, one CTA per (run, KV head, query), and its raw tail is one more run.
+// The cut depends on the row's own length only, so the bits of an output do not
+// depend on the batch.  Selected rows (at most 512 groups): runs of 32 groups.
+// Whole histories: longer runs for longer rows, so that the partial states stay
+// a small part of the codes read (n_q/n_kv * (d+2) * 4 bytes per run against
+// run_groups * 8*d), doubled beyond 65,536 groups to keep at most 512 runs.
+constexpr int kCodedRunRows = 32;
+
+__host__ __device__ inline int coded_run_groups(int groups, bool whole)
+{
+    if (!whole || groups <= 1024) return kCodedRunRows;
+    if (groups <= 4096) return 64;
+    int r = 128;
+    while ((groups + r - 1) / r > 512) r *= 2;
+    return r;
+}
+
+// Upper bound of the runs (the tail's included) of any row of at most
+// max_groups complete groups.
+inline int coded_max_runs(int max_groups, bool whole)
+{
+    auto runs = [&](int g) {
+        const int r = coded_run_groups(g, whole);
+        return (g + r - 1) / r;
+    };
+    int n = runs(max_groups);
+    if (whole) {  // the counts at the ends of the ranges that share a run length
+        for (int edge = 1024; edge < max_groups; edge *= 2) n = n > runs(edge) ? n : runs(edge);
+    }
+    return n + 1;
+}
+
+struct CodedLayout {
+    Layout base;
+    int nparts;           // partial states per (query, head)
+    int mass_stride;      // group shares per (query, head); a multiple of 4
+    size_t off_part_m, off_part_l, off_part_acc;  // [B, n_q, nparts], acc with d floats each
+    size_t off_mass;      // [B, n_q, mass_stride]: sum of e^(x - mref) of each group
+    size_t off_mref;      // [B, n_q, mass_stride/4]: the reference of four groups
+    size_t off_stat;      // [B, n_q, 2]: the row's maximum and 1/denominator
+    size_t off_bad;       // [B]: the row may not add weights
+    size_t total;
+};
+CodedLayout make_coded_layout(const qsa_dims *d, bool whole, bool weights);
+
+struct CodeArgs {
+    const float *k_cache, *v_cache;
+    int64_t num_slots;
+    const int32_t *slot_map;
+    const int64_t *slot_offset;
+    const int32_t *group_begin, *group_end;
+    uint8_t *codes;
+    float *scales;
+    int64_t num_blocks;
+    const int32_t *block_map;
+    const int64_t *block_offset;
+    int32_t format, batch, kv_heads, head_dim, max_groups, g_max;
+    uint32_t *err;
+};
+cudaError_t launch_code_groups(const CodeArgs &a, cudaStream_t s);
+
+struct AttendCodedArgs {
+    const float *q;
+    const int32_t *visible;
+    const int32_t *ids, *n_ids;     // nullptr: whole histories
+    int32_t *ids_out, *n_ids_out;   // the caller's copy of the rows (nullptr: not wanted)
+    const uint8_t *codes;
+    const float *scales;
+    int64_t num_blocks;
+    const int32_t *block_map;
+    const int64_t *block_offset;
+    const float *k_cache, *v_cache;
+    int64_t num_slots;
+    const int32_t *slot_map;
+    const int64_t *slot_offset;
+    float *out;
+    float *part_m, *part_l, *part_acc;
+    float *mass, *mref, *stat;      // nullptr: no weights
+    uint32_t *bad;
+    float *weights;
+    const int64_t *weight_offset;
+    int32_t format, batch, q_heads, kv_heads, head_dim, row_cap, nparts, mass_stride, max_visible;
+    float scale;
+    uint32_t *err;
+};
+bool attend_coded_shape_supported(int head_dim, int q_heads, int kv_heads);
+cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s, bool pdl);
+
+struct EvictSelectArgs {
+    const int32_t *visible;
+    const float *weights;
+    const int64_t *weight_offset;
+    int32_t *kept, *n_kept, *evicted;
+    int32_t batch, max_visible, keep, sink, recent;
+    uint32_t *err;
+};
+cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t s);
+
+struct EvictCompactArgs {
+    const int32_t *kept, *n_kept;
+    qsa_history src, dst;
+    int32_t batch, max_visible, keep, idx_dim;
+    uint32_t *err;
+};
+cudaError_t launch_evict_compact(const EvictCompactArgs &a, int num_sms, cudaStream_t s);
+
+// api.cu: qsa_score_groups / qsa_score_pooled and qsa_select as qsa_decode runs
+// them (rows and counts to the workspace, selection hints, overlapped launches).
+qsa_status score_and_select(const qsa_dims *d, const qsa_inputs *in, const float *pooled, const int64_t *pool_offset,
+                            void *ws, const Layout &L, cudaStream_t s);
+int num_sms_of_current_device();
+
+}  // namespace qsa

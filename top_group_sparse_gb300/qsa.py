@@ -24,6 +24,8 @@ __all__ = [
     "DeviceBatch",
     "QSA_DEVERR_VISIBLE_RANGE", "QSA_DEVERR_SLOT_RANGE", "QSA_DEVERR_ROW_RANGE", "QSA_DEVERR_NOT_SHARED",
     "QSA_DEVERR_WAIT_TIMEOUT",
+    "QsaCodedCache", "QsaHistory", "qsa_code_groups", "qsa_coded_workspace_size", "qsa_attend_coded",
+    "qsa_decode_coded", "qsa_evict_select", "qsa_evict_compact", "QSA_CODE_E4M3", "QSA_CODE_INT8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +38,8 @@ QSA_DEVERR_SLOT_RANGE = 0x2
 QSA_DEVERR_ROW_RANGE = 0x4
 QSA_DEVERR_WAIT_TIMEOUT = 0x8
 QSA_DEVERR_NOT_SHARED = 0x10
+QSA_CODE_E4M3 = 0
+QSA_CODE_INT8 = 1
 
 
 class QsaError(RuntimeError):
@@ -69,8 +73,33 @@ class QsaStats(ctypes.Structure):
         return {n: int(getattr(self, n)) for n, _ in self._fields_}
 
 
+class QsaCodedCache(ctypes.Structure):
+    """qsa_coded_cache (include/qsa_cache.h)."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("block_map", ctypes.c_void_p), ("block_offset", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+    @classmethod
+    def of(cls, codes, scales, block_map, block_offset, fmt):
+        """From tensors: codes [num_blocks, n_kv, 8*d] (uint8), scales [num_blocks, n_kv, 2]."""
+        return cls(_ptr(codes), _ptr(scales), int(codes.shape[0]), _ptr(block_map), _ptr(block_offset), int(fmt))
+
+
+class QsaHistory(ctypes.Structure):
+    """qsa_history (include/qsa_cache.h)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "idx_keys", "key_offset", "pooled", "pool_offset", "slot_map", "slot_offset", "block_map", "block_offset",
+        "weights", "weight_offset", "visible")]
+
+    @classmethod
+    def of(cls, **members):
+        """From tensors by member name; members left out are NULL."""
+        return cls(**{k: _ptr(v) for k, v in members.items()})
+
+
 _lib = None
 _P = ctypes.c_void_p
+_CP = ctypes.POINTER(QsaCodedCache)
+_HP = ctypes.POINTER(QsaHistory)
 _DP = ctypes.POINTER(QsaDims)
 _IP = ctypes.POINTER(QsaInputs)
 
@@ -139,6 +168,19 @@ def load(path: str | None = None):
     L.qsa_decode_shared.restype = ctypes.c_int
     L.qsa_probe_ffma.argtypes = [ctypes.c_int32, ctypes.c_int32, _P, ctypes.POINTER(ctypes.c_int64), _P]
     L.qsa_probe_ffma.restype = ctypes.c_int
+    L.qsa_coded_workspace_size.argtypes = [_DP, ctypes.c_int32, ctypes.c_int32]
+    L.qsa_coded_workspace_size.restype = ctypes.c_size_t
+    L.qsa_code_groups.argtypes = [_DP, _IP, _CP, _P, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]
+    L.qsa_code_groups.restype = ctypes.c_int
+    L.qsa_attend_coded.argtypes = [_DP, _IP, _CP, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+    L.qsa_attend_coded.restype = ctypes.c_int
+    L.qsa_decode_coded.argtypes = [_DP, _IP, _CP, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]
+    L.qsa_decode_coded.restype = ctypes.c_int
+    L.qsa_evict_select.argtypes = [_DP, _P, _P, _P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P,
+                                   ctypes.c_size_t, _P]
+    L.qsa_evict_select.restype = ctypes.c_int
+    L.qsa_evict_compact.argtypes = [_DP, ctypes.c_int32, _P, _P, _HP, _HP, _P, ctypes.c_size_t, _P]
+    L.qsa_evict_compact.restype = ctypes.c_int
     if path is None:
         _lib = L
     return L
@@ -373,6 +415,55 @@ def qsa_attend_noalloc(dims, q, k_scr, v_scr, n_ids, out, stream=None) -> int:
     workspace, for callers that cannot allocate device memory."""
     return _check("qsa_attend_noalloc", load().qsa_attend_noalloc(
         ctypes.byref(dims), _ptr(q), _ptr(k_scr), _ptr(v_scr), _ptr(n_ids), _ptr(out),
+        _stream(stream)))
+
+
+# ---- the coded cache and the eviction (include/qsa_cache.h) ------------------
+
+def qsa_coded_workspace_size(dims, whole_history=False, with_weights=False) -> int:
+    return int(load().qsa_coded_workspace_size(ctypes.byref(dims), int(bool(whole_history)), int(bool(with_weights))))
+
+
+def qsa_code_groups(dims, inputs, cache, group_begin, group_end, max_groups, ws, stream=None) -> int:
+    """Codes groups [group_begin[b], group_end[b]) of every query into its blocks of the coded cache."""
+    p, n = _ws(ws)
+    return _check("qsa_code_groups", load().qsa_code_groups(
+        ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(cache), _ptr(group_begin), _ptr(group_end),
+        int(max_groups), p, n, _stream(stream)))
+
+
+def qsa_attend_coded(dims, inputs, cache, ids, n_ids, out, ws, weights=None, weight_offset=None, stream=None) -> int:
+    """Attention over the coded cache: over the rows ids[b, :n_ids[b]], or (ids = n_ids = None) over every
+    visible token; weights: the accumulators that the groups' shares of attention are added to."""
+    p, n = _ws(ws)
+    return _check("qsa_attend_coded", load().qsa_attend_coded(
+        ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(cache), _ptr(ids), _ptr(n_ids), _ptr(out),
+        _ptr(weights), _ptr(weight_offset), p, n, _stream(stream)))
+
+
+def qsa_decode_coded(dims, inputs, cache, ids, n_ids, out, ws, pooled=None, pool_offset=None, weights=None,
+                     weight_offset=None, stream=None) -> int:
+    """The whole path over a coded cache, scored from the pooled-key cache when `pooled` is given."""
+    p, n = _ws(ws)
+    return _check("qsa_decode_coded", load().qsa_decode_coded(
+        ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(cache), _ptr(pooled), _ptr(pool_offset), _ptr(ids),
+        _ptr(n_ids), _ptr(out), _ptr(weights), _ptr(weight_offset), p, n, _stream(stream)))
+
+
+def qsa_evict_select(dims, visible, weights, weight_offset, keep_groups, sink_groups, recent_groups, kept, n_kept, ws,
+                     evicted=None, stream=None) -> int:
+    """The groups each history keeps: kept [B, keep_groups] ascending, n_kept [B]; evicted: the others."""
+    p, n = _ws(ws)
+    return _check("qsa_evict_select", load().qsa_evict_select(
+        ctypes.byref(dims), _ptr(visible), _ptr(weights), _ptr(weight_offset), int(keep_groups), int(sink_groups),
+        int(recent_groups), _ptr(kept), _ptr(n_kept), _ptr(evicted), p, n, _stream(stream)))
+
+
+def qsa_evict_compact(dims, keep_groups, kept, n_kept, src, dst, ws, stream=None) -> int:
+    """Moves the kept groups of the histories `src` to `dst` (QsaHistory each)."""
+    p, n = _ws(ws)
+    return _check("qsa_evict_compact", load().qsa_evict_compact(
+        ctypes.byref(dims), int(keep_groups), _ptr(kept), _ptr(n_kept), ctypes.byref(src), ctypes.byref(dst), p, n,
         _stream(stream)))
 
 
