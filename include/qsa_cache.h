@@ -74,7 +74,7 @@ qsa_status qsa_code_groups(const qsa_dims *dims, const qsa_inputs *in, const qsa
  * are invalid): qsa_workspace_size(dims) when both flags are 0, followed by
  *   whole_history: the attention's partial states, n_q*(d+2) floats per run of
  *     a row and query, at most 514 runs;
- *   with_weights: n_q * (1.25 * groups of a row + 2) floats per query, groups =
+ *   with_weights: n_q * (1.25 * groups of a row + 2) + 2 floats per query, groups =
  *     max_visible/4 for whole histories, else budget_groups.
  * Linear in the history, never queries x keys of other queries.  A workspace
  * made for both flags serves every call of this library with these dims. */
@@ -98,7 +98,7 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * += sum over heads h and over the row's tokens t of group g = t/4 of
  * softmax(x)_t, the incomplete last group (g = visible[b]/4) included, so one
  * query adds n_q in all.  Queries with the same weight_offset share a history:
- * their shares are added in batch order, so the sum has one value (the rows of
+ * their shares are added in a fixed order, so the sum has one value (the rows of
  * different offsets must not overlap).
  *
  * The codes are exact in 16-bit floats; q and the softmax weights enter the

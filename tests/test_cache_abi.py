@@ -69,9 +69,9 @@ def test_workspace_closed_forms(lib):
     # 1,024 groups: 32 runs of 32, and the tail's
     part = 2 * up(heads * 33 * 4) + up(heads * 33 * 128 * 4)
     assert qsa.qsa_coded_workspace_size(d, True, False) == base + part
-    mass = up(heads * 1024 * 4) + up(heads * 256 * 4) + up(heads * 8) + up(2 * 4)
+    mass = up(heads * 1024 * 4) + up(heads * 256 * 4) + up(heads * 8) + 2 * up(2 * 4)
     assert qsa.qsa_coded_workspace_size(d, True, True) == base + part + mass
-    rows = up(heads * 512 * 4) + up(heads * 128 * 4) + up(heads * 8) + up(2 * 4)
+    rows = up(heads * 512 * 4) + up(heads * 128 * 4) + up(heads * 8) + 2 * up(2 * 4)
     assert qsa.qsa_coded_workspace_size(d, False, True) == base + rows
     # the longest history: at most 512 runs and the tail's, whatever its length
     d = _dims(batch=1, max_visible=1 << 26)

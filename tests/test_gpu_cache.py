@@ -184,7 +184,7 @@ def test_attention_over_selected_rows(budget, fmt, q_heads, kv, d):
 @pytest.mark.parametrize("whole", [True, False])
 def test_weights_of_a_shared_history_are_added_in_batch_order(whole):
     torch = need_gpu()
-    vis = [997 + i for i in range(37)]
+    vis = [989 + i for i in range(39)]  # up to 1,027: 256 groups and a tail of 3
     h = ch.History(vis, q_heads=8, kv_heads=2, head_dim=64, fmt=ch.INT8, seed=14, shared=True)
     t = ch.device(h, budget=64, whole=whole, weights=True)
     ch.fill_cache(h, t)
@@ -201,6 +201,37 @@ def test_weights_of_a_shared_history_are_added_in_batch_order(whole):
         t["weights"].copy_(torch.from_numpy(h.weights0))
         _attend(t, ids, n, weights=True)
         assert torch.equal(t["weights"], again)
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_weights_of_several_shared_histories_in_one_batch(whole):
+    """600 queries: five histories dealt out in turn (sharers far apart, beyond one
+    block of 256), and some queries with accumulators of their own among them."""
+    torch = need_gpu()
+    r = np.random.RandomState(24)
+    B = 600
+    h = ch.History([int(t) for t in r.randint(1, 90, B)], q_heads=2, kv_heads=1, head_dim=64, fmt=ch.E4M3, seed=25)
+    room = 24  # groups per accumulator row
+    own = r.rand(B) < 0.1
+    pick = np.where(own, 5 + np.arange(B), np.arange(B) % 5)
+    pick[300:560][~own[300:560]] = 2
+    h.weight_offset = (pick * room).astype(np.int64)
+    h.n_weights = (5 + B) * room
+    h.weights0 = r.rand(h.n_weights).astype(np.float32)
+    rows = None if whole else ch.some_rows(h, 9, 26)
+    t = ch.device(h, budget=9, whole=whole, weights=True)
+    ch.fill_cache(h, t)
+    ids, n = (None, None) if whole else ch.rows_to_device(rows, 9)
+    _, share, _, rel = ch.attention(h, rows)
+    _attend(t, ids, n, weights=True)
+    _ok(t)
+    w, wt = ch.add_weights(h, share, rel)
+    got = t["weights"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()
+    again = t["weights"].clone()
+    t["weights"].copy_(torch.from_numpy(h.weights0))
+    _attend(t, ids, n, weights=True)
+    assert torch.equal(t["weights"], again)
 
 
 def test_an_output_does_not_depend_on_the_batch_or_the_workspace():

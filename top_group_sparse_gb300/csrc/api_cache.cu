@@ -38,8 +38,11 @@ CodedLayout make_coded_layout(const qsa_dims *d, bool whole, bool weights)
         off = align_up(off + heads * size_t(C.mass_stride / 4) * 4, kWsAlign);
         C.off_stat = off;
         off = align_up(off + heads * 8, kWsAlign);
-        C.off_bad = off;
+        C.off_sharing = off;
         off = align_up(off + size_t(d->batch) * 4, kWsAlign);
+        C.off_tail = off;
+        off = align_up(off + size_t(d->batch) * 4, kWsAlign);
+        C.map_stride = int(C.base.score_stride);
     }
     C.total = off;
     return C;
@@ -120,7 +123,10 @@ AttendCodedArgs attend_args(const qsa_dims *d, const qsa_inputs *in, const qsa_c
         a.mass = at<float>(ws, C.off_mass);
         a.mref = at<float>(ws, C.off_mref);
         a.stat = at<float>(ws, C.off_stat);
-        a.bad = at<uint32_t>(ws, C.off_bad);
+        a.sharing = at<uint32_t>(ws, C.off_sharing);
+        a.share_map = at<float>(ws, C.base.off_scores);
+        a.tail_share = at<float>(ws, C.off_tail);
+        a.map_stride = C.map_stride;
         a.weights = weights;
         a.weight_offset = weight_offset;
     }

@@ -15,13 +15,14 @@ namespace qsa {
 // Whole histories: longer runs for longer rows, so that the partial states stay
 // a small part of the codes read (n_q/n_kv * (d+2) * 4 bytes per run against
 // run_groups * 8*d), doubled beyond 65,536 groups to keep at most 512 runs.
-constexpr int kCodedRunRows = 32;
+constexpr int kCodedRunRows = 64;
 
 __host__ __device__ inline int coded_run_groups(int groups, bool whole)
 {
-    if (!whole || groups <= 1024) return kCodedRunRows;
-    if (groups <= 4096) return 64;
-    int r = 128;
+    if (!whole) return kCodedRunRows;
+    if (groups <= 1024) return 32;
+    if (groups <= 4096) return 128;
+    int r = 256;
     while ((groups + r - 1) / r > 512) r *= 2;
     return r;
 }
@@ -49,7 +50,9 @@ struct CodedLayout {
     size_t off_mass;      // [B, n_q, mass_stride]: sum of e^(x - mref) of each group
     size_t off_mref;      // [B, n_q, mass_stride/4]: the reference of four groups
     size_t off_stat;      // [B, n_q, 2]: the row's maximum and 1/denominator
-    size_t off_bad;       // [B]: the row may not add weights
+    size_t off_sharing;   // [B]: whether the row may add weights, and to accumulators of its own
+    size_t off_tail;      // [B]: the raw tail's share, where accumulators are shared
+    int map_stride;       // selected rows: [B, map_stride] shares by group, in the scores' place
     size_t total;
 };
 CodedLayout make_coded_layout(const qsa_dims *d, bool whole, bool weights);
@@ -87,10 +90,11 @@ struct AttendCodedArgs {
     float *out;
     float *part_m, *part_l, *part_acc;
     float *mass, *mref, *stat;      // nullptr: no weights
-    uint32_t *bad;
+    uint32_t *sharing;
+    float *share_map, *tail_share;
     float *weights;
     const int64_t *weight_offset;
-    int32_t format, batch, q_heads, kv_heads, head_dim, row_cap, nparts, mass_stride, max_visible;
+    int32_t format, batch, q_heads, kv_heads, head_dim, row_cap, nparts, mass_stride, map_stride, max_visible;
     float scale;
     uint32_t *err;
 };

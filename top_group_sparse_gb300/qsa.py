@@ -207,8 +207,9 @@ def _ptr(x) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
+        # the current stream's handle without a Stream object around it: 0.3 us instead of 3 us
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
