@@ -14,7 +14,7 @@ CodedLayout make_coded_layout(const qsa_dims *d, bool whole, bool weights)
     const size_t heads = size_t(d->batch) * size_t(d->q_heads);
     size_t off = C.base.total;
     if (whole) {
-        C.nparts = coded_max_runs(g_max, true);
+        C.nparts = coded_max_runs(g_max, true, d->q_heads / d->kv_heads) + 1;
         C.off_part_m = off;
         off = align_up(off + heads * size_t(C.nparts) * 4, kWsAlign);
         C.off_part_l = off;
@@ -124,7 +124,7 @@ AttendCodedArgs attend_args(const qsa_dims *d, const qsa_inputs *in, const qsa_c
         a.mref = at<float>(ws, C.off_mref);
         a.stat = at<float>(ws, C.off_stat);
         a.sharing = at<uint32_t>(ws, C.off_sharing);
-        a.share_map = at<float>(ws, C.base.off_scores);
+        if (d->batch > 1) a.share_map = at<float>(ws, C.base.off_scores);  // (one query shares with nobody)
         a.tail_share = at<float>(ws, C.off_tail);
         a.map_stride = C.map_stride;
         a.weights = weights;

@@ -8,43 +8,53 @@
 namespace qsa {
 
 // ---- how a row is cut ---------------------------------------------------------
-// A row of n complete groups is cut into runs of run_groups(n) consecutive
-// groups, one CTA per (run, KV head, query), and its raw tail is one more run.
-// The cut depends on the row's own length only, so the bits of an output do not
-// depend on the batch.  Selected rows (at most 512 groups): runs of 32 groups.
-// Whole histories: longer runs for longer rows, so that the partial states stay
-// a small part of the codes read (n_q/n_kv * (d+2) * 4 bytes per run against
-// run_groups * 8*d), doubled beyond 65,536 groups to keep at most 512 runs.
+// A row of n complete groups is cut into runs of coded_run_groups(n) consecutive
+// groups, one CTA per (run, KV head, query), and its raw tail is one more run, the
+// last.  The cut depends on the row's own length and on the heads per KV
+// head only, so the bits of an output do not depend on the batch.  Shorter runs
+// spread a row over more SMs, longer ones pay less for a CTA's start and for the
+// partial states (n_q/n_kv * (d+2) * 4 bytes per run against 8*d per group).
+// Measured, whole histories of 32 ragged rows of up to 16,384 groups (8 heads):
+// runs of 128 take 95 us, of 256 84 us; 4 rows of 10,000 groups with 16 heads:
+// 21 and 27 us; 12 rows of up to 2,250 groups: runs of 64 16 us, of 128 18 us.
+// Selected rows (at most 512 groups), 256 queries: runs of 32 85 us, of 64 68 us;
+// 8 queries: 6.1 us both.  Beyond 65,536 groups the length doubles so that a row has
+// at most 512 runs.
 constexpr int kCodedRunRows = 64;
 
-__host__ __device__ inline int coded_run_groups(int groups, bool whole)
+__host__ __device__ inline int coded_run_groups(int groups, bool whole, int heads_per_kv)
 {
     if (!whole) return kCodedRunRows;
     if (groups <= 1024) return 32;
-    if (groups <= 4096) return 128;
-    int r = 256;
+    if (groups <= 4096) return 64;
+    int r = heads_per_kv > 8 ? 128 : 256;
     while ((groups + r - 1) / r > 512) r *= 2;
     return r;
 }
 
-// Upper bound of the runs (the tail's included) of any row of at most
-// max_groups complete groups.
-inline int coded_max_runs(int max_groups, bool whole)
+// Upper bound of the runs (the tail's not included) of any row of at most max_groups complete groups.
+inline int coded_max_runs(int max_groups, bool whole, int heads_per_kv)
 {
     auto runs = [&](int g) {
-        const int r = coded_run_groups(g, whole);
+        const int r = coded_run_groups(g, whole, heads_per_kv);
         return (g + r - 1) / r;
     };
     int n = runs(max_groups);
     if (whole) {  // the counts at the ends of the ranges that share a run length
         for (int edge = 1024; edge < max_groups; edge *= 2) n = n > runs(edge) ? n : runs(edge);
     }
-    return n + 1;
+    return n;
+}
+
+__host__ __device__ inline int coded_runs(int groups, bool whole, int heads_per_kv)
+{
+    const int per = coded_run_groups(groups, whole, heads_per_kv);
+    return (groups + per - 1) / per;
 }
 
 struct CodedLayout {
     Layout base;
-    int nparts;           // partial states per (query, head)
+    int nparts;           // partial states per (query, head): the runs and the tail
     int mass_stride;      // group shares per (query, head); a multiple of 4
     size_t off_part_m, off_part_l, off_part_acc;  // [B, n_q, nparts], acc with d floats each
     size_t off_mass;      // [B, n_q, mass_stride]: sum of e^(x - mref) of each group
@@ -99,6 +109,7 @@ struct AttendCodedArgs {
     uint32_t *err;
 };
 bool attend_coded_shape_supported(int head_dim, int q_heads, int kv_heads);
+cudaError_t launch_merge_coded(const AttendCodedArgs &a, cudaStream_t s);  // after the runs' states
 cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s, bool pdl);
 
 struct EvictSelectArgs {
@@ -124,5 +135,39 @@ cudaError_t launch_evict_compact(const EvictCompactArgs &a, int num_sms, cudaStr
 qsa_status score_and_select(const qsa_dims *d, const qsa_inputs *in, const float *pooled, const int64_t *pool_offset,
                             void *ws, const Layout &L, cudaStream_t s);
 int num_sms_of_current_device();
+
+// ---- device helpers ----------------------------------------------------------
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x; results below the smallest normal float are 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// of AttendCodedArgs::sharing: the row may not add weights; the first, or a later,
+// of several queries that add to one history's accumulators
+constexpr uint32_t kBad = 1u, kFirstSharer = 2u, kLaterSharer = 4u;
+
+// Query b's row.  ok: its count and T_b are in range (else it is empty).
+struct Row {
+    int groups, tail;   // complete groups; raw tokens behind them
+    int T;              // visible tokens
+    bool t_ok, ok;
+};
+__device__ __forceinline__ Row row_of(const AttendCodedArgs &a, int b)
+{
+    Row r;
+    r.T = __ldg(a.visible + b);
+    const int n = a.ids != nullptr ? __ldcg(a.n_ids + b) : r.T;
+    r.t_ok = r.T >= 0 && r.T <= a.max_visible;
+    r.ok = r.t_ok && n >= 0 && (a.ids == nullptr || n <= a.row_cap);
+    r.groups = r.ok ? n / kGroup : 0;
+    r.tail = r.ok ? n % kGroup : 0;
+    return r;
+}
 
 }  // namespace qsa

@@ -1,0 +1,406 @@
+// merge_coded.cu -- the second half of qsa_attend_coded (include/qsa_cache.h):
+// the states of a row's runs merged, and the attention that each group received
+// added to its accumulator.
+#include <type_traits>
+
+#include "cache_internal.cuh"
+
+namespace qsa {
+namespace {
+
+// ---- the runs of a row merged in run order -----------------------------------------------
+// Per (query, head): M = max m_c, w_c = 2^(m_c - M), L = sum l_c w_c, out = sum
+// acc_c w_c / L, c over the runs (the raw tail's is the last).
+//
+// Rows of at most 32 runs: a warp per head and 64 dims, eight a CTA.  Longer ones: a
+// CTA per head.  Both add in the same order -- eight sums over the runs c = s,
+// s+8, .. (s < 8), added in order of s -- so that a row's bits do not depend on
+// which of the two its batch takes.  Latency bound: every load that can be is
+// made before the first is used.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kSlices = 8;
+constexpr int kWarpRuns = 32;
+constexpr int kMaxRuns = 513;
+constexpr int kRunsPerThread = (kMaxRuns + kMergeThreads - 1) / kMergeThreads;
+
+template <int D>
+using Vec = typename std::conditional<D == 128, float4, float2>::type;  // a lane's dims
+template <typename V>
+__device__ __forceinline__ float at(const V &v, int j) { return reinterpret_cast<const float *>(&v)[j]; }
+template <typename V>
+__device__ __forceinline__ float &at(V &v, int j) { return reinterpret_cast<float *>(&v)[j]; }
+
+__device__ __forceinline__ int used_runs(const AttendCodedArgs &a, const Row &row)
+{
+    return coded_runs(row.groups, a.ids == nullptr, a.q_heads / a.kv_heads) + (row.tail > 0 ? 1 : 0);
+}
+
+__device__ __forceinline__ float inverse(float L)  // of a denominator; 0: no token (or none above -inf)
+{
+    return L > 0.0f || L != L ? 1.0f / L : 0.0f;
+}
+
+// Unit u: 64 dims of head u / (D/64), two a lane.
+template <int D>
+__device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, int u, const Row &row)
+{
+    constexpr int kPer = 2;
+    constexpr int kHalves = D / 64;
+    const int h = u / kHalves, col = (u % kHalves) * 32 + (threadIdx.x & 31);
+    const int lane = threadIdx.x & 31;
+    const int used = used_runs(a, row);
+    const int64_t hb = int64_t(b) * a.q_heads + h;
+    const float2 *src = reinterpret_cast<const float2 *>(a.part_acc + hb * a.nparts * D) + col;
+    const float pm = lane < used ? __ldcg(a.part_m + hb * a.nparts + lane) : -INFINITY;
+    const float pl = lane < used ? __ldcg(a.part_l + hb * a.nparts + lane) : 0.0f;
+    float2 x[kSlices];
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s)
+        if (s < used) x[s] = __ldcg(src + int64_t(s) * (D / 2));
+    float m = pm;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float M = m == -INFINITY ? 0.0f : m;
+    const float w = lane < used ? ex2(pm - M) : 0.0f;
+    float L = lane < used ? fmaf(pl, w, 0.0f) : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float sum[kSlices][kPer];
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum[s][j] = 0.0f;
+    for (int c0 = 0; c0 < used; c0 += kSlices) {
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, w, (c0 + s) & 31);
+            if (c0 + s < used) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) sum[s][j] = fmaf(at(x[s], j), ws, sum[s][j]);
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s)
+            if (c0 + kSlices + s < used) x[s] = __ldcg(src + int64_t(c0 + kSlices + s) * (D / 2));
+    }
+    float2 out;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        float o = sum[0][j];
+#pragma unroll
+        for (int s = 1; s < kSlices; ++s) o += sum[s][j];
+        at(out, j) = L > 0.0f || L != L ? o / L : 0.0f;
+    }
+    reinterpret_cast<float2 *>(a.out + hb * D)[col] = out;
+    if (a.stat != nullptr && col == 0) reinterpret_cast<float2 *>(a.stat)[hb] = make_float2(M, inverse(L));
+}
+
+template <int D>
+__device__ __forceinline__ void merge_by_block(const AttendCodedArgs &a, int b, int h, const Row &row)
+{
+    constexpr int kPer = D / 32;
+    constexpr int kAhead = 8;
+    __shared__ float w[kMaxRuns];
+    __shared__ float red[2][kMergeWarps];
+    __shared__ Vec<D> part[kSlices][32];
+    static_assert(kMergeWarps == kSlices, "a warp per slice");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int used = used_runs(a, row);
+    const int64_t hb = int64_t(b) * a.q_heads + h;
+    const Vec<D> *src = reinterpret_cast<const Vec<D> *>(a.part_acc + hb * a.nparts * D) + lane;
+    float pm[kRunsPerThread], pl[kRunsPerThread];
+#pragma unroll
+    for (int k = 0; k < kRunsPerThread; ++k) {
+        const int c = tid + k * kMergeThreads;
+        pm[k] = c < used ? __ldcg(a.part_m + hb * a.nparts + c) : -INFINITY;
+        pl[k] = c < used ? __ldcg(a.part_l + hb * a.nparts + c) : 0.0f;
+    }
+    Vec<D> x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+        if (warp + u * kSlices < used) x[u] = __ldcg(src + int64_t(warp + u * kSlices) * 32);
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kRunsPerThread; ++k) m = fmaxf(m, pm[k]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMergeWarps; ++k) m = fmaxf(m, red[0][k]);
+    const float M = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kRunsPerThread; ++k) {
+        const int c = tid + k * kMergeThreads;
+        if (c >= used) continue;
+        w[c] = ex2(pm[k] - M);
+        l = fmaf(pl[k], w[c], l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    float L = red[1][0];
+#pragma unroll
+    for (int k = 1; k < kMergeWarps; ++k) L += red[1][k];
+    float o[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) o[j] = 0.0f;
+    for (int c0 = warp; c0 < used; c0 += kAhead * kSlices) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + u * kSlices;
+            if (c < used) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) o[j] = fmaf(at(x[u], j), w[c], o[j]);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int c = c0 + (kAhead + u) * kSlices;
+            if (c < used) x[u] = __ldcg(src + int64_t(c) * 32);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) at(part[warp][lane], j) = o[j];
+    __syncthreads();
+    if (warp != 0) return;
+    Vec<D> out;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        float y = o[j];
+#pragma unroll
+        for (int s = 1; s < kSlices; ++s) y += at(part[s][lane], j);
+        at(out, j) = L > 0.0f || L != L ? y / L : 0.0f;
+    }
+    reinterpret_cast<Vec<D> *>(a.out + hb * D)[lane] = out;
+    if (a.stat != nullptr && lane == 0) reinterpret_cast<float2 *>(a.stat)[hb] = make_float2(M, inverse(L));
+}
+
+// ---- the groups' shares of attention ------------------------------------------------------
+// weights[weight_offset[b] + g] += sum_h share(b, h, g), share = mass * 2^(mref - M_h) / L_h.
+// No atomics: a query with accumulators of its own adds its shares as they come
+// (own_weights, CTAs beside the merge's, which find M and L themselves from the
+// runs' states rather than wait for the merge); queries that share accumulators
+// are added in a fixed order, eight threads per group (shared_weights_kernel), so
+// that the sum has one value.  Selected rows of such queries are first spread out
+// to one share per group of the history (in the workspace's scores, which nobody
+// needs by then), so that the second kernel reads rows side by side: on 256
+// queries that share a history of 25,064 groups, searching each group in each
+// query's row instead took 1540 us, this 16 us.
+constexpr int kAccThreads = kMergeThreads;
+constexpr int kOwnPos = kAccThreads;                   // positions of a CTA, one per thread
+constexpr int kStatHeads = 64;                         // heads whose M and 1/L are in hand at a time
+constexpr int kSharedSlices = 8;                       // threads per group, an eighth of the queries each
+constexpr int kSharedGroups = kAccThreads / kSharedSlices;
+
+// M and 1/L of a head from its runs' states, by a warp.
+__device__ __forceinline__ float2 stat_of_runs(const AttendCodedArgs &a, int64_t hb, int used)
+{
+    const float *pm = a.part_m + hb * a.nparts, *pl = a.part_l + hb * a.nparts;
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+    for (int c = threadIdx.x & 31; c < used; c += 32) {
+        const float mc = __ldcg(pm + c), lc = __ldcg(pl + c);
+        const float mn = fmaxf(m, mc);
+        const float ms = mn == -INFINITY ? 0.0f : mn;
+        l = fmaf(l, ex2(m - ms), lc * ex2(mc - ms));
+        m = mn;
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.0f;
+    l *= ex2(m - M);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    return make_float2(M, inverse(l));
+}
+
+// CTA `x` of `n` for query b.
+__device__ __forceinline__ void own_weights(const AttendCodedArgs &a, int b, int x, int n, const Row &row)
+{
+    __shared__ float2 stat[kStatHeads];
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const bool whole = a.ids == nullptr;
+    const uint32_t sharing = __ldcg(a.sharing + b);
+    const bool own = sharing == 0;
+    // (shared accumulators of whole histories: shared_weights_kernel reads the masses itself)
+    const int first = !own && whole ? row.groups : 0, end = row.groups + (row.tail > 0 ? 1 : 0);
+    if ((sharing & kBad) || first + int64_t(x) * kOwnPos >= end) return;
+    const int used = used_runs(a, row);
+    const int64_t hb0 = int64_t(b) * a.q_heads;
+    for (int64_t p0 = first + int64_t(x) * kOwnPos; p0 < end; p0 += int64_t(n) * kOwnPos) {
+        const int p = int(p0) + tid;
+        int g = row.T / kGroup;
+        if (p < row.groups) g = whole ? p : __ldcg(a.ids + int64_t(b) * a.row_cap + kGroup * int64_t(p)) / kGroup;
+        float s = 0.0f;
+        for (int h0 = 0; h0 < a.q_heads; h0 += kStatHeads) {
+            const int nh = min(kStatHeads, a.q_heads - h0);
+            if (p0 == first + int64_t(x) * kOwnPos || a.q_heads > kStatHeads) {
+                __syncthreads();
+#pragma unroll 2
+                for (int h = warp; h < nh; h += kMergeWarps) {
+                    const float2 st = stat_of_runs(a, hb0 + h0 + h, used);
+                    if (tid % 32 == 0) stat[h] = st;
+                }
+                __syncthreads();
+            }
+            if (p >= end) continue;
+            const float *mass = a.mass + (hb0 + h0) * a.mass_stride + p;
+            const float *mref = a.mref + (hb0 + h0) * (a.mass_stride / 4) + p / 4;
+            int64_t ms = a.mass_stride, rs = a.mass_stride / 4;
+            if (p == row.groups) {  // the raw tail: its run's state
+                mass = a.part_l + (hb0 + h0) * a.nparts + used - 1;
+                mref = a.part_m + (hb0 + h0) * a.nparts + used - 1;
+                ms = rs = a.nparts;
+            }
+#pragma unroll 8
+            for (int h = 0; h < nh; ++h)
+                s = fmaf(__ldcg(mass + h * ms) * ex2(__ldcg(mref + h * rs) - stat[h].x), stat[h].y, s);
+        }
+        if (p >= end) continue;
+        if (own) a.weights[__ldg(a.weight_offset + b) + g] += s;
+        else if (p == row.groups) a.tail_share[b] = s;
+        else a.share_map[int64_t(b) * a.map_stride + g] = s;
+    }
+}
+
+template <int D, bool kByWarp>
+__global__ void __launch_bounds__(kMergeThreads, 4) merge_coded_kernel(const AttendCodedArgs a, int merge_ctas)
+{
+    const int x = blockIdx.x, b = blockIdx.y;
+    wait_for_predecessor();
+    const Row row = row_of(a, b);
+    if (x >= merge_ctas) {
+        own_weights(a, b, x - merge_ctas, int(gridDim.x) - merge_ctas, row);
+    } else if constexpr (kByWarp) {
+        const int u = x * kMergeWarps + (threadIdx.x >> 5);
+        if (u < a.q_heads * (D / 64)) merge_by_warp<D>(a, b, u, row);
+    } else {
+        merge_by_block<D>(a, b, x, row);
+    }
+}
+
+// Heads h0, h0 + step, .. of position pos.
+__device__ __forceinline__ float share_of(const AttendCodedArgs &a, int b, int pos, int h0, int step)
+{
+    float s = 0.0f;
+    const int64_t hb = int64_t(b) * a.q_heads;
+    const float *mass = a.mass + hb * a.mass_stride + pos;
+    const float *mref = a.mref + hb * (a.mass_stride / 4) + pos / 4;
+    const float2 *stat = reinterpret_cast<const float2 *>(a.stat) + hb;
+#pragma unroll 4
+    for (int h = h0; h < a.q_heads; h += step) {
+        const float2 st = __ldcg(stat + h);
+        const float g = __ldcg(mass + int64_t(h) * a.mass_stride);
+        const float r = __ldcg(mref + int64_t(h) * (a.mass_stride / 4));
+        s = fmaf(g * ex2(r - st.x), st.y, s);
+    }
+    return s;
+}
+
+template <bool kWhole>
+__global__ void __launch_bounds__(kAccThreads) shared_weights_kernel(const AttendCodedArgs a)
+{
+    __shared__ int2 member[kAccThreads];  // per query: complete groups of its history (-1: adds nothing here), tail
+    __shared__ float sum[kSharedSlices][kSharedGroups];
+    __shared__ uint32_t first_of[kAccThreads / 32];
+    constexpr int kAhead = 16;            // shares loaded before they are added
+    const int tid = threadIdx.x, lg = tid % kSharedGroups, slice = tid / kSharedGroups;
+    const int groups = a.max_visible / kGroup + 1;
+    wait_for_predecessor();
+    for (int b0 = 0; b0 < a.batch; b0 += kAccThreads) {
+        const bool first = b0 + tid < a.batch && (__ldcg(a.sharing + b0 + tid) & kFirstSharer);
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        if (!__syncthreads_or(first)) continue;
+        if (tid % 32 == 0) first_of[tid / 32] = firsts;
+        __syncthreads();
+        for (int i = 0; i < kAccThreads; ++i) {  // the histories' first queries
+            const uint32_t left = first_of[i / 32] >> (i % 32);
+            if (left == 0) {  // none in the rest of the 32
+                i |= 31;
+                continue;
+            }
+            i += __ffs(left) - 1;
+            const int b = b0 + i;
+            const int64_t off = __ldg(a.weight_offset + b);
+            for (int64_t g0 = int64_t(blockIdx.x) * kSharedGroups; g0 < groups; g0 += int64_t(gridDim.x) * kSharedGroups) {
+                const int g = int(g0) + lg;
+                float s = 0.0f;
+                for (int o0 = b; o0 < a.batch; o0 += kAccThreads) {
+                    const int n = min(kAccThreads, a.batch - o0);
+                    __syncthreads();
+                    member[tid] = make_int2(-1, 0);
+                    if (tid < n && __ldg(a.weight_offset + o0 + tid) == off && !(__ldcg(a.sharing + o0 + tid) & kBad)) {
+                        const Row row = row_of(a, o0 + tid);
+                        member[tid] = make_int2(row.T / kGroup, row.tail);
+                    }
+                    __syncthreads();
+                    if constexpr (kWhole) {
+                        for (int j = slice; j < n; j += kSharedSlices)
+                            if (g < member[j].x) s += share_of(a, o0 + j, g, 0, 1);
+                    } else {
+                        for (int j = slice; j < n; j += kSharedSlices * kAhead) {
+                            float t[kAhead];
+#pragma unroll
+                            for (int u = 0; u < kAhead; ++u) {
+                                const int o = min(j + u * kSharedSlices, n - 1);  // (every load is made, no branch between them)
+                                t[u] = __ldcg(a.share_map + int64_t(o0 + o) * a.map_stride + min(g, a.map_stride - 1));
+                            }
+#pragma unroll
+                            for (int u = 0; u < kAhead; ++u) {
+                                const int o = j + u * kSharedSlices;
+                                if (o < n && g < member[o].x) s += t[u];
+                            }
+                        }
+                    }
+                    for (int j = slice; j < n; j += kSharedSlices)  // the raw tails
+                        if (member[j].x == g && member[j].y > 0) s += __ldcg(a.tail_share + o0 + j);
+                }
+                sum[slice][lg] = s;
+                __syncthreads();
+                if (slice == 0) {
+#pragma unroll
+                    for (int k = 1; k < kSharedSlices; ++k) s += sum[k][lg];
+                    if (s != 0.0f) a.weights[off + g] += s;
+                }
+                __syncthreads();
+            }
+        }
+        __syncthreads();  // first_of is filled again
+    }
+}
+
+template <int D>
+cudaError_t launch_merge_t(const AttendCodedArgs &a, cudaStream_t s)
+{
+    int own = 0;
+    if (a.weights != nullptr) {
+        const int positions = (a.ids == nullptr ? a.max_visible : a.row_cap) / kGroup + 1;
+        own = (positions + kOwnPos - 1) / kOwnPos;
+        if (own > 1024) own = 1024;
+    }
+    if (a.nparts <= kWarpRuns) {
+        const int ctas = (a.q_heads * (D / 64) + kMergeWarps - 1) / kMergeWarps;
+        return launch_kernel(merge_coded_kernel<D, true>, dim3(unsigned(ctas + own), unsigned(a.batch)), dim3(kMergeThreads), 0, s,
+                             true, a, ctas);
+    }
+    return launch_kernel(merge_coded_kernel<D, false>, dim3(unsigned(a.q_heads + own), unsigned(a.batch)), dim3(kMergeThreads), 0,
+                         s, true, a, a.q_heads);
+}
+
+}  // namespace
+
+cudaError_t launch_merge_coded(const AttendCodedArgs &a, cudaStream_t s)
+{
+    cudaError_t e = a.head_dim == 128 ? launch_merge_t<128>(a, s) : launch_merge_t<64>(a, s);
+    if (e != cudaSuccess || a.weights == nullptr || a.batch == 1) return e;
+    const int blocks = (a.max_visible / kGroup + kSharedGroups) / kSharedGroups;
+    return launch_kernel(a.ids == nullptr ? shared_weights_kernel<true> : shared_weights_kernel<false>,
+                         dim3(unsigned(blocks < 1024 ? blocks : 1024)), dim3(kAccThreads), 0, s, true, a);
+}
+
+}  // namespace qsa
