@@ -97,6 +97,38 @@ def test_coding_of_extreme_groups(fmt, d):
         assert np.array_equal(got[blk], c)
 
 
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("log2_scale", [-120, -89, -40, 0, 3, 100])
+def test_codes_next_to_the_borders_between_codes(fmt, log2_scale):
+    """Values at, and one or two units beside, the middle of two codes: the rounded
+    quotient decides, and a quotient that is off by one unit shows."""
+    need_gpu()
+    r = np.random.RandomState(8)
+    n, d = 400, 64
+    h = ch.History([4 * n], q_heads=1, kv_heads=1, head_dim=d, fmt=fmt, seed=9)
+    grid = np.unique(np.abs(ch.e4m3_table()[:0x7f])) if fmt == ch.E4M3 else np.arange(128.0)
+    mid = (grid[1:] + grid[:-1]) / 2
+    for a in (h.k, h.v):
+        amax = (2.0 ** log2_scale * (1 + r.rand(n))).astype(np.float32)
+        s = amax * (np.float32(1) / np.float32(ch.QMAX[fmt]))
+        x = (mid[r.randint(0, len(mid), (n, 4 * d))] * s[:, None].astype(np.float64)).astype(np.float32)
+        x = (x.view(np.int32) + r.randint(-2, 3, x.shape).astype(np.int32)).view(np.float32) * r.choice([-1, 1], x.shape).astype(np.float32)
+        x = np.clip(x, -amax[:, None], amax[:, None])
+        x[np.arange(n), r.randint(0, 4 * d, n)] = amax
+        a[:] = x.reshape(4 * n, 1, d)
+    h.k_cache[h.slot_map], h.v_cache[h.slot_map] = h.k, h.v
+    t = ch.device(h)
+    ch.fill_cache(h, t)
+    _ok(t)
+    K, V = ch.unpack(t["codes"].cpu().numpy(), d, fmt)
+    s = t["scales"].cpu().numpy()
+    blk = h.block_map[:n]
+    for src, got, j in ((h.k, K, 0), (h.v, V, 1)):
+        c, sc = ch.encode(src.reshape(n, 4, 1, d).transpose(0, 2, 1, 3), fmt)
+        assert np.array_equal(s[blk, :, j], sc)
+        assert np.array_equal(got[blk], c)
+
+
 def test_coding_flags_and_skips_what_is_out_of_range():
     torch = need_gpu()
     from top_group_sparse_gb300 import qsa

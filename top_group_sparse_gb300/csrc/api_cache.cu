@@ -187,7 +187,7 @@ qsa_status qsa_attend_coded(const qsa_dims *dims, const qsa_inputs *in, const qs
     const CodedLayout C = make_coded_layout(dims, ids == nullptr, weights != nullptr);
     if ((st = check_ws(ws, ws_bytes, C.total)) != QSA_OK) return st;
     const AttendCodedArgs a = attend_args(dims, in, cache, ids, n_ids, out, weights, weight_offset, ws, C);
-    return from_cuda(launch_attend_coded(a, static_cast<cudaStream_t>(stream), false));
+    return from_cuda(launch_attend_coded(a, static_cast<cudaStream_t>(stream), true));
 }
 
 qsa_status qsa_decode_coded(const qsa_dims *dims, const qsa_inputs *in, const qsa_coded_cache *cache,

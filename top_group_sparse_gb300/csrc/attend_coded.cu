@@ -48,7 +48,8 @@ struct Sm {
     static constexpr int kStage = kStepGroups * kBlk;
     alignas(128) unsigned char ring[kWarps][kRing][kStage];  // also the end-of-run reduction area
     alignas(16) float4 meta[kSegGroups];                     // K scale, V scale * f, 1/f, 0 (-inf: no such group)
-    alignas(16) uint4 qa[HS == 2 ? D / 16 : 1][2][HS == 2 ? 32 : 1];  // 9-16 heads: each lane's operands of q, hi and lo
+    alignas(16) uint4 qa[D / 16][HS][32];                    // each lane's operands of q (9-16 heads: hi, lo)
+    float qs[8 * HS];                                        // 1/f of each head's q
     alignas(16) int blk[kSegGroups];                         // physical block; -1: none, -2: zero rows
     float wm[kWarps][8 * HS], wl[kWarps][8 * HS];
 };
@@ -401,66 +402,61 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
     first_steps(my_steps);
     const float2 my_scales = load_scales(my_blk);
 
-    // ---- the queries: the matrix operands of each 16 dims, hi and lo ---------------------
-    // hi and lo words of dims 4u..4u+3 of the 16 that lane (head hl + 8*s, i4) holds of
-    // half j, with the head's power of two taken out
-    auto q_scale = [&](int s, float &f, float &inv) {
-        uint32_t top = 0;
-        const int h = hl + 8 * s;
+    // ---- the queries: 16 threads a head, each 8 dims at a time, to the matrix operands -----
+    // of the lane that holds the dims: words of dims 4u..4u+3 of 64j + 16*i4, hi and lo,
+    // with the head's power of two taken out
+    constexpr int kQPer = D / 128 > 0 ? D / 128 : 1;   // pieces of 8 dims per thread and head
+    constexpr int kQThreads = D / 8 / kQPer;           // threads per head: 16, or 8 for d = 64
+#pragma unroll
+    for (int h0q = 0; h0q < 8 * HS; h0q += kThreads / kQThreads) {
+        const int h = h0q + tid / kQThreads, c = tid % kQThreads;  // dims 8c..8c+7
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         if (h < gq) {
-            const float4 *src = reinterpret_cast<const float4 *>(a.q + (int64_t(b) * a.q_heads + h0 + h) * D + 16 * i4);
-#pragma unroll
-            for (int j = 0; j < kHalves; ++j)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float4 x = __ldg(src + 16 * j + u);
-                    top = max(top, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
-                    top = max(top, max(__float_as_uint(x.z) & 0x7fffffffu, __float_as_uint(x.w) & 0x7fffffffu));
-                }
+            const float4 *src = reinterpret_cast<const float4 *>(a.q + (int64_t(b) * a.q_heads + h0 + h) * D) + 2 * c;
+            x = __ldg(src);
+            y = __ldg(src + 1);
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        uint32_t top = 0;
+        for (const float v : {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w}) top = max(top, __float_as_uint(v) & 0x7fffffffu);
+#pragma unroll
+        for (int o = 1; o < kQThreads; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float f, inv;
         scale_to<kQTop>(top, f, inv);
-    };
-    auto q_words = [&](int s, int j, int u, float f, uint32_t (&hi)[2], uint32_t (&lo)[2]) {
-        const int h = hl + 8 * s;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h < gq)
-            x = __ldg(reinterpret_cast<const float4 *>(a.q + (int64_t(b) * a.q_heads + h0 + h) * D + 64 * j + 16 * i4) + u);
+        if (h >= 8 * HS) continue;  // (d = 64: more threads than heads need)
+        uint32_t hi[4], lo[4];
         split2(make_float2(x.x * f, x.y * f), hi[0], lo[0]);
         split2(make_float2(x.z * f, x.w * f), hi[1], lo[1]);
-    };
-    uint32_t qa[HS == 1 ? kHalves : 1][4][4];  // (up to 8 heads: in registers)
-    float hscale[HS], qf[HS];
+        split2(make_float2(y.x * f, y.y * f), hi[2], lo[2]);
+        split2(make_float2(y.z * f, y.w * f), hi[3], lo[3]);
+        const int e = 4 * (c / 8) + 2 * (c % 2), to = (h % 8) * 4 + (c % 8) / 2;
 #pragma unroll
-    for (int s = 0; s < HS; ++s) {
-        float inv;
-        q_scale(s, qf[s], inv);
-        hscale[s] = a.scale * kLog2e * inv;
+        for (int u = 0; u < 2; ++u) {
+            if constexpr (HS == 1) {
+                sm.qa[e + u][0][to] = make_uint4(hi[2 * u], lo[2 * u], hi[2 * u + 1], lo[2 * u + 1]);
+            } else {  // rows hl and hl + 8 of an operand are heads: the second set's words are y and w
+                uint32_t *const ph = reinterpret_cast<uint32_t *>(&sm.qa[e + u][0][to]) + h / 8;
+                uint32_t *const pl = reinterpret_cast<uint32_t *>(&sm.qa[e + u][HS - 1][to]) + h / 8;
+                ph[0] = hi[2 * u], ph[2] = hi[2 * u + 1];
+                pl[0] = lo[2 * u], pl[2] = lo[2 * u + 1];
+            }
+        }
+        if (c == 0) sm.qs[h] = inv;
     }
+    store_meta(my_blk, my_scales);
+    __syncthreads();
+    uint32_t qa[HS == 1 ? kHalves : 1][4][4];  // (up to 8 heads: in registers)
     if constexpr (HS == 1) {
 #pragma unroll
         for (int j = 0; j < kHalves; ++j)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                uint32_t hi[2], lo[2];
-                q_words(0, j, u, qf[0], hi, lo);
-                qa[j][u][0] = hi[0];
-                qa[j][u][1] = lo[0];
-                qa[j][u][2] = hi[1];
-                qa[j][u][3] = lo[1];
+                const uint4 v = sm.qa[4 * j + u][0][lane];
+                qa[j][u][0] = v.x, qa[j][u][1] = v.y, qa[j][u][2] = v.z, qa[j][u][3] = v.w;
             }
-    } else {
-        for (int e = warp; e < kHalves * 4; e += kWarps) {
-            uint32_t hi[2][2], lo[2][2];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) q_words(s, e / 4, e % 4, qf[s], hi[s], lo[s]);
-            sm.qa[e][0][lane] = make_uint4(hi[0][0], hi[1][0], hi[0][1], hi[1][1]);
-            sm.qa[e][1][lane] = make_uint4(lo[0][0], lo[1][0], lo[0][1], lo[1][1]);
-        }
     }
-    store_meta(my_blk, my_scales);
-    __syncthreads();
+    float hscale[HS];
+#pragma unroll
+    for (int s = 0; s < HS; ++s) hscale[s] = a.scale * kLog2e * sm.qs[hl + 8 * s];
 
     // the accumulator: dims 32*j + 8*i4 + u (x) and + 4 (y) of head hl + 8*s
     float2 acc[HS][kVC][4];
@@ -629,53 +625,58 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
         }
         cp_async_wait<0>();
     }
-    __syncthreads();  // every warp is done with the ring
-
-    // ---- the run's state: the warps' states merged in warp order ------------------------
-    float *red = reinterpret_cast<float *>(sm.ring);  // [kWarps][kNH][D]
+    // ---- the run's state: the warps' accumulators brought to one maximum and added in warp order
 #pragma unroll
     for (int s = 0; s < HS; ++s) {
-        const int h = hl + 8 * s;
-#pragma unroll
-        for (int j = 0; j < kVC; ++j) {
-            float4 *dst = reinterpret_cast<float4 *>(red + (warp * kNH + h) * D + 32 * j + 8 * i4);
-            dst[0] = make_float4(acc[s][j][0].x, acc[s][j][1].x, acc[s][j][2].x, acc[s][j][3].x);
-            dst[1] = make_float4(acc[s][j][0].y, acc[s][j][1].y, acc[s][j][2].y, acc[s][j][3].y);
-        }
         float l = l_run[s];
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (i4 == 0) {
-            sm.wm[warp][h] = m_run[s];
-            sm.wl[warp][h] = l;
+            sm.wm[warp][hl + 8 * s] = m_run[s];
+            sm.wl[warp][hl + 8 * s] = l;
         }
     }
-    __syncthreads();
+    __syncthreads();  // (and every warp is done with the ring)
+    float *red = reinterpret_cast<float *>(sm.ring);  // [kWarps][kNH][D]
     const int64_t pbase = (int64_t(b) * a.q_heads + h0) * a.nparts + part;  // of the first head
-    constexpr int F4 = D / 4;
-    for (int e = tid; e < gq * F4; e += kThreads) {
-        const int h = e / F4, c = e % F4;
+#pragma unroll
+    for (int s = 0; s < HS; ++s) {
+        const int h = hl + 8 * s;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.wm[w][h]);
         const float Ms = M == -INFINITY ? 0.0f : M;
-        float L = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float wt = ex2(m_run[s] - Ms);
+        if (warp == 0 && i4 == 0 && h < gq) {
+            float L = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float wt = ex2(sm.wm[w][h] - Ms);
-            L = fmaf(sm.wl[w][h], wt, L);
-            const float4 p = *reinterpret_cast<const float4 *>(red + (w * kNH + h) * D + 4 * c);
-            o.x = fmaf(p.x, wt, o.x);
-            o.y = fmaf(p.y, wt, o.y);
-            o.z = fmaf(p.z, wt, o.z);
-            o.w = fmaf(p.w, wt, o.w);
-        }
-        reinterpret_cast<float4 *>(a.part_acc + (pbase + int64_t(h) * a.nparts) * D)[c] = o;
-        if (c == 0) {
+            for (int w = 0; w < kWarps; ++w) L = fmaf(sm.wl[w][h], ex2(sm.wm[w][h] - Ms), L);
             a.part_m[pbase + int64_t(h) * a.nparts] = M;
             a.part_l[pbase + int64_t(h) * a.nparts] = L;
         }
+#pragma unroll
+        for (int j = 0; j < kVC; ++j) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) acc[s][j][u] = mul2(acc[s][j][u], wt);
+            float4 *dst = reinterpret_cast<float4 *>(red + (warp * kNH + h) * D + 32 * j + 8 * i4);
+            dst[0] = make_float4(acc[s][j][0].x, acc[s][j][1].x, acc[s][j][2].x, acc[s][j][3].x);
+            dst[1] = make_float4(acc[s][j][0].y, acc[s][j][1].y, acc[s][j][2].y, acc[s][j][3].y);
+        }
+    }
+    __syncthreads();
+    constexpr int F4 = D / 4;
+    for (int e = tid; e < gq * F4; e += kThreads) {
+        const int h = e / F4, c = e % F4;
+        float4 o = *reinterpret_cast<const float4 *>(red + h * D + 4 * c);
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 p = *reinterpret_cast<const float4 *>(red + (w * kNH + h) * D + 4 * c);
+            o.x += p.x;
+            o.y += p.y;
+            o.z += p.z;
+            o.w += p.w;
+        }
+        reinterpret_cast<float4 *>(a.part_acc + (pbase + int64_t(h) * a.nparts) * D)[c] = o;
     }
 }
 

@@ -18,46 +18,69 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Two floats to e4m3 codes, round to nearest even, the lower one first.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+// The largest of |a|, |b| and |c|; NaN if one of them is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
 {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
     return r;
 }
 
+// x / s rounded to nearest, given r = 1/s rounded to nearest.  The first two steps
+// bring q within one unit in the last place of the quotient; then, by Markstein's
+// theorem (P. Markstein, Computation of elementary functions on the IBM RISC
+// System/6000, 1990), one more correction by the exact remainder rounds as the
+// division does.  A remainder is exact while it does not underflow: the caller
+// divides where the scale is below 2^-90 (and a quotient so small that its own
+// remainder underflows is far below half the smallest code).
+__device__ __forceinline__ float quotient(float x, float s, float r)
+{
+    float q = __fmul_rn(x, r);
+    q = __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+}
+
+// Four quotients of at most the format's largest code in size, as codes.
 template <bool kInt8>
 __device__ __forceinline__ uint32_t code4(float x, float y, float z, float w)
 {
     if constexpr (kInt8) {
-        auto c = [](float v) { return uint32_t(max(-127, min(127, __float2int_rn(v)))) & 0xffu; };
-        return c(x) | (c(y) << 8) | (c(z) << 16) | (c(w) << 24);
+        // x + 1.5 * 2^23 rounds x to the nearest integer, even on ties, and holds it in its low bits
+        constexpr float kMagic = 12582912.0f;
+        const uint32_t lo = __byte_perm(__float_as_uint(__fadd_rn(x, kMagic)), __float_as_uint(__fadd_rn(y, kMagic)), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(__fadd_rn(z, kMagic)), __float_as_uint(__fadd_rn(w, kMagic)), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
     } else {
-        return e4m3x2(x, y) | (e4m3x2(z, w) << 16);
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y), "f"(x));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(w), "f"(z));
+        return uint32_t(lo) | (uint32_t(hi) << 16);
     }
 }
 
-// Codes the four tokens' rows of K or V of one (group, head), kLanes lanes of 4
+// Codes the four tokens' rows of K or V of one (group, head), D/4 lanes of 4
 // dims each: r[u] are this lane's dims (4*l .. 4*l+3) of token u.  Every lane of
 // the warp calls it (two halves may code different rows).
 template <int D, bool kInt8>
 __device__ __forceinline__ void code_rows(const float4 (&r)[4], int l, bool is_k, uint8_t *dst, float *scale_dst)
 {
-    uint32_t top = 0;  // bits of the largest |x|: a NaN's are above infinity's, infinity's above every number's
+    float top = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        top = max(top, __float_as_uint(r[u].x) & 0x7fffffffu);
-        top = max(top, __float_as_uint(r[u].y) & 0x7fffffffu);
-        top = max(top, __float_as_uint(r[u].z) & 0x7fffffffu);
-        top = max(top, __float_as_uint(r[u].w) & 0x7fffffffu);
-    }
+    for (int u = 0; u < 4; ++u) top = max_abs3(max_abs3(top, r[u].x, r[u].y), r[u].z, r[u].w);
+    uint32_t bits = __float_as_uint(top);  // (a NaN's are above infinity's, infinity's above every number's)
 #pragma unroll
-    for (int o = D / 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const bool finite = top < 0x7f800000u;
-    float s = __fmul_rn(__uint_as_float(top), kInt8 ? 1.0f / 127.0f : 1.0f / 448.0f);
+    for (int o = D / 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+    const bool finite = bits < 0x7f800000u;
+    float s = __fmul_rn(__uint_as_float(bits), kInt8 ? 1.0f / 127.0f : 1.0f / 448.0f);
     if (s < 1.17549435e-38f) s = 0.0f;  // below the smallest normal float: flushed
     uint32_t c[4] = {0u, 0u, 0u, 0u};
-    if (finite && s > 0.0f) {
+    if (finite && s > 0x1p-90f) {
+        const float inv = __frcp_rn(s);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            c[u] = code4<kInt8>(quotient(r[u].x, s, inv), quotient(r[u].y, s, inv), quotient(r[u].z, s, inv),
+                                quotient(r[u].w, s, inv));
+    } else if (finite && s > 0.0f) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
             c[u] = code4<kInt8>(__fdiv_rn(r[u].x, s), __fdiv_rn(r[u].y, s), __fdiv_rn(r[u].z, s), __fdiv_rn(r[u].w, s));
@@ -81,6 +104,7 @@ __global__ void __launch_bounds__(kThreads) code_groups_kernel(const CodeArgs a)
 {
     const int b = blockIdx.y;
     const int lane = threadIdx.x & 31;
+    wait_for_predecessor();
     const int g_begin = __ldg(a.group_begin + b), g_end = __ldg(a.group_end + b);
     if (g_begin < 0 || g_end < g_begin || g_end > a.g_max || g_end - g_begin > a.max_groups) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, QSA_DEVERR_VISIBLE_RANGE);
@@ -136,16 +160,10 @@ cudaError_t launch_code_groups(const CodeArgs &a, cudaStream_t s)
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     const dim3 grid(unsigned(blocks), unsigned(a.batch));
     const bool i8 = a.format == QSA_CODE_INT8;
-    if (a.head_dim == 128) {
-        if (i8) code_groups_kernel<128, true><<<grid, kThreads, 0, s>>>(a);
-        else code_groups_kernel<128, false><<<grid, kThreads, 0, s>>>(a);
-    } else if (a.head_dim == 64) {
-        if (i8) code_groups_kernel<64, true><<<grid, kThreads, 0, s>>>(a);
-        else code_groups_kernel<64, false><<<grid, kThreads, 0, s>>>(a);
-    } else {
-        return cudaErrorInvalidValue;
-    }
-    return cudaGetLastError();
+    auto launch = [&](void (*kernel)(const CodeArgs)) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, true, a); };
+    if (a.head_dim == 128) return launch(i8 ? code_groups_kernel<128, true> : code_groups_kernel<128, false>);
+    if (a.head_dim == 64) return launch(i8 ? code_groups_kernel<64, true> : code_groups_kernel<64, false>);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace qsa

@@ -25,14 +25,14 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kPer = 4;                     // consecutive positions per thread in the emission
+constexpr int kPer = 8;                     // consecutive positions per thread in the emission
 constexpr int kCached = 40960;              // keys a CTA keeps in shared memory at most
 constexpr int kCluster = 8;
+constexpr int kOneCta = 4096;               // histories of up to so many groups: one CTA, no cluster
 
 struct SelectSmem {
-    uint32_t hist[kBins];
+    alignas(16) uint32_t hist[3][kBins];    // one per pass: a pass needs no barrier behind the others' reads
     uint32_t warp_sum[2][kWarps];
-    uint32_t above, equal;                  // this slice's keys above and equal to K
     uint32_t bin, rest;
 };
 
@@ -76,13 +76,15 @@ __device__ __forceinline__ void block_scan2(SelectSmem &sm, uint32_t &x, uint32_
     y += py - y0;
 }
 
+template <int kRanks>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelectArgs a, int cached)
 {
     extern __shared__ __align__(16) uint32_t keys[];  // [cached]
     __shared__ SelectSmem sm;
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = int(cluster.block_rank()), nr = int(cluster.num_blocks());
+    const int rank = kRanks == 1 ? 0 : int(cluster.block_rank());
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    wait_for_predecessor();
     const int T = __ldg(a.visible + b);
     if (T < 0 || T > a.max_visible) {  // (the whole cluster leaves)
         if (rank == 0 && tid == 0) {
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
     int32_t *kept = a.kept + int64_t(b) * a.keep;
     if (rank == 0 && tid == 0) a.n_kept[b] = min(G, a.keep);
     if (G <= a.keep) {
-        for (int g = rank * kThreads + tid; g < G; g += nr * kThreads) kept[g] = g;
+        for (int g = rank * kThreads + tid; g < G; g += kRanks * kThreads) kept[g] = g;
         return;
     }
     int32_t *evicted = a.evicted != nullptr ? a.evicted + int64_t(b) * (a.max_visible / kGroup) : nullptr;
@@ -103,54 +105,77 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
     const int lo = a.sink, n = G - a.sink - a.recent;
     const uint32_t need = uint32_t(a.keep - a.sink - a.recent);
     const float *w = a.weights + __ldg(a.weight_offset + b) + lo;
-    const int slice = ((n + nr - 1) / nr + kPer - 1) / kPer * kPer;
+    const int slice = ((n + kRanks - 1) / kRanks + kPer - 1) / kPer * kPer;
     const int s0 = min(n, rank * slice), sn = min(n, s0 + slice) - s0;
     const bool in_smem = sn <= cached;
     if (in_smem) {
+#pragma unroll 8
         for (int i = tid; i < sn; i += kThreads) keys[i] = weight_key(__ldg(w + s0 + i));
-        __syncthreads();
     }
     auto key_at = [&](int i) { return in_smem ? keys[i] : weight_key(__ldg(w + s0 + i)); };
+#pragma unroll
+    for (int i = 0; i < 3 * kBins / kThreads; ++i) sm.hist[0][tid + i * kThreads] = 0;
+    __syncthreads();
 
-    // ---- K, the need-th largest key, and how many keys equal to it are kept ---------
+    // ---- K, the need-th largest key, and how many keys equal to it are kept; the keys
+    // above and equal to K in the slices before this one ----------------------------------
     uint32_t K = 0xffffffffu, ties = 0;  // (no key is that large: nothing is kept)
+    uint32_t base_gt = 0, base_eq = 0;
     if (need > 0) {
         uint32_t rest = need, prefix = 0;
         int shift = 21, bits = 11;
+#pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            for (int i = tid; i < kBins; i += kThreads) sm.hist[i] = 0;
-            __syncthreads();
+            uint32_t *my_hist = sm.hist[pass];
             const uint32_t above_mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
+#pragma unroll 4
             for (int i0 = 0; i0 < sn; i0 += kThreads) {
                 const int i = i0 + tid;
                 const uint32_t k = i < sn ? key_at(i) : 0u;
                 const bool in = i < sn && (k & above_mask) == prefix;
+                if (!__any_sync(0xffffffffu, in)) continue;
                 // many groups weigh the same (nothing, above all): a warp's equal bins are counted once
                 const uint32_t bin = in ? (k >> shift) & ((1u << bits) - 1u) : 0xffffffffu;
                 const uint32_t same = __match_any_sync(0xffffffffu, bin);
-                if (in && lane == __ffs(same) - 1) atomicAdd(&sm.hist[bin], uint32_t(__popc(same)));
+                if (in && lane == __ffs(same) - 1) atomicAdd(&my_hist[bin], uint32_t(__popc(same)));
             }
-            cluster.sync();
+            if constexpr (kRanks == 1) __syncthreads();
+            else cluster.sync();
             // the counts of the whole history, from the top bin down: a thread takes four bins
-            uint32_t c[kBins / kThreads], mine = 0, none = 0, total, unused;
+            constexpr int kMine = kBins / kThreads;
+            static_assert(kMine == 4, "a thread's bins are one 16-byte piece");
+            const int first_bin = kBins - kMine * (tid + 1);
+            uint4 v[kRanks];
 #pragma unroll
-            for (int j = 0; j < kBins / kThreads; ++j) {
-                const int bin = kBins - 1 - (tid * (kBins / kThreads) + j);
-                uint32_t sum = 0;
-                for (int r = 0; r < nr; ++r) sum += cluster.map_shared_rank(sm.hist, r)[bin];
-                c[j] = sum;
-                mine += sum;
-            }
-            block_scan2(sm, mine, none, total, unused);  // mine: keys in the bins above this thread's
+            for (int r = 0; r < kRanks; ++r)
+                v[r] = *reinterpret_cast<const uint4 *>((kRanks == 1 ? my_hist : cluster.map_shared_rank(my_hist, r)) + first_bin);
+            uint32_t c[kMine] = {0, 0, 0, 0}, before[kMine] = {0, 0, 0, 0};  // of all slices, of the slices before this one
 #pragma unroll
-            for (int j = 0; j < kBins / kThreads; ++j) {
-                if (mine < rest && rest <= mine + c[j]) {  // exactly one bin of one thread
-                    sm.bin = uint32_t(kBins - 1 - (tid * (kBins / kThreads) + j));
-                    sm.rest = rest - mine;
+            for (int r = 0; r < kRanks; ++r) {
+                const uint32_t x[kMine] = {v[r].w, v[r].z, v[r].y, v[r].x};
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    c[j] += x[j];
+                    if (r < rank) before[j] += x[j];
                 }
-                mine += c[j];
             }
-            cluster.sync();  // every CTA has read the counts (and sm.bin is set)
+            uint32_t above = (c[0] + c[1]) + (c[2] + c[3]), none = 0, total, unused;
+            block_scan2(sm, above, none, total, unused);  // above: keys in the bins above this thread's
+            uint32_t gt = 0, eq = 0;
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                if (above + c[j] < rest) gt += before[j];  // a bin above K's
+                if (above < rest && rest <= above + c[j]) {  // K's bin: exactly one bin of one thread
+                    sm.bin = uint32_t(first_bin + kMine - 1 - j);
+                    sm.rest = rest - above;
+                    if (pass == 2) eq = before[j];
+                }
+                above += c[j];
+            }
+            uint32_t tg, te;
+            block_scan2(sm, gt, eq, tg, te);  // (also: sm.bin is there)
+            base_gt += tg;
+            base_eq = te;
             prefix |= sm.bin << shift;
             rest = sm.rest;
             bits = pass == 1 ? 10 : 11;
@@ -159,35 +184,25 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
         K = prefix;
         ties = rest;
     }
-
-    // ---- counts of the lower slices ----------------------------------------------------
-    uint32_t gt = 0, eq = 0, tg, te;
-    for (int i = tid; i < sn; i += kThreads) {
-        const uint32_t k = key_at(i);
-        gt += k > K;
-        eq += k == K;
-    }
-    block_scan2(sm, gt, eq, tg, te);
-    if (tid == 0) {
-        sm.above = tg;
-        sm.equal = te;
-    }
-    cluster.sync();
-    uint32_t base_gt = 0, base_eq = 0;
-    for (int r = 0; r < rank; ++r) {
-        const SelectSmem *o = cluster.map_shared_rank(&sm, r);
-        base_gt += o->above;
-        base_eq += o->equal;
-    }
+    // no CTA leaves while another may read its counts: this one has read the others'
+    if constexpr (kRanks > 1) cluster.barrier_arrive();
 
     // ---- emission in ascending position ------------------------------------------------
     for (int i0 = 0; i0 < sn; i0 += kThreads * kPer) {
         const int first = i0 + tid * kPer;
-        uint32_t k[kPer];
-        gt = eq = 0;
+        uint32_t k[kPer], gt = 0, eq = 0, tg, te;
+        if (in_smem) {  // (16-byte reads; what is behind the slice is not used)
+#pragma unroll
+            for (int j = 0; j < kPer; j += 4) {
+                const uint4 x = first + j < sn ? *reinterpret_cast<const uint4 *>(keys + first + j) : make_uint4(0, 0, 0, 0);
+                k[j] = x.x, k[j + 1] = x.y, k[j + 2] = x.z, k[j + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) k[j] = first + j < sn ? weight_key(__ldg(w + s0 + first + j)) : 0u;
+        }
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            k[j] = first + j < sn ? key_at(first + j) : 0u;
             if (first + j < sn) {
                 gt += k[j] > K;
                 eq += k[j] == K;
@@ -213,16 +228,21 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
         for (int g = tid; g < a.sink; g += kThreads) kept[g] = g;
         for (int j = tid; j < a.recent; j += kThreads) kept[a.keep - a.recent + j] = G - a.recent + j;
     }
-    cluster.sync();  // no CTA leaves while another may read its shared memory
+    if constexpr (kRanks > 1) cluster.barrier_wait();
 }
 
 // ---- the move ------------------------------------------------------------------------
 // Bound by memory: every kept row read once and written once (10*d_I*4 bytes of
-// keys and 48 of maps and weights per group).  A warp takes a group: a lane's
-// 16-byte pieces of the four raw rows and of the pooled row are all loaded
-// before the first is stored.
+// keys and 48 of maps and weights per group).  A warp takes kTake groups at a
+// time: a lane's 16-byte pieces of all their rows are loaded before the first is
+// stored, and the next groups' positions while they are on their way.  Eight
+// histories of 65,536 groups cut to half: 24 CTAs per SM 104 us (6.6 TB/s), 16 107
+// us, 12 109 us; one CTA per 8 groups, each with its three dependent loads before
+// the first row, 117 us.
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / 32;
+constexpr int kTake = 2;
+constexpr int kMoveCtas = 24;               // per SM, over the whole batch
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const EvictCompactArgs a)
@@ -230,6 +250,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Evict
     constexpr int F4 = D / 4;               // 16-byte pieces of a row
     constexpr int kRaw = kGroup * F4 / 32;  // of the four raw rows, per lane
     const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    wait_for_predecessor();
     const int T = __ldg(a.src.visible + b), n = __ldg(a.n_kept + b);
     const int G = T / kGroup, tail = T % kGroup;
     if (T < 0 || T > a.max_visible || n < 0 || n > a.keep || n > G) {
@@ -239,99 +260,131 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Evict
         }
         return;
     }
+    // query b's regions (16-byte pieces for the keys); a member that is not moved stays NULL
     const qsa_history &s = a.src, &d = a.dst;
-    if (blockIdx.x == 0) {
-        if (tid == 0) d.visible[b] = kGroup * n + tail;
-        if (tid < tail) {
-            if (s.slot_map != nullptr)
-                d.slot_map[__ldg(d.slot_offset + b) + kGroup * int64_t(n) + tid] =
-                    __ldg(s.slot_map + __ldg(s.slot_offset + b) + kGroup * int64_t(G) + tid);
-        }
-        if (s.idx_keys != nullptr && tid < tail * F4)
-            reinterpret_cast<float4 *>(d.idx_keys + (__ldg(d.key_offset + b) + kGroup * int64_t(n)) * D)[tid] =
-                __ldg(reinterpret_cast<const float4 *>(s.idx_keys + (__ldg(s.key_offset + b) + kGroup * int64_t(G)) * D) + tid);
-        if (s.weights != nullptr && tail > 0 && tid == 0)
-            d.weights[__ldg(d.weight_offset + b) + n] = __ldg(s.weights + __ldg(s.weight_offset + b) + G);
+    auto region = [&](auto *p, const int64_t *offset, int64_t row) { return p == nullptr ? p : p + __ldg(offset + b) * row; };
+    const float4 *s_raw = reinterpret_cast<const float4 *>(region(s.idx_keys, s.key_offset, D));
+    float4 *d_raw = reinterpret_cast<float4 *>(region(d.idx_keys, d.key_offset, D));
+    const float4 *s_pool = reinterpret_cast<const float4 *>(region(s.pooled, s.pool_offset, D));
+    float4 *d_pool = reinterpret_cast<float4 *>(region(d.pooled, d.pool_offset, D));
+    // a lane's entry of the maps and weights, as 32-bit words: lanes 0-3 the slots of a
+    // group, lane 4 its block, lane 5 its weight
+    const uint32_t *s_map = nullptr;
+    uint32_t *d_map = nullptr;
+    int per = 0;  // words per group
+    if (lane < kGroup && s.slot_map != nullptr) {
+        s_map = reinterpret_cast<const uint32_t *>(region(s.slot_map, s.slot_offset, 1)) + lane;
+        d_map = reinterpret_cast<uint32_t *>(region(d.slot_map, d.slot_offset, 1)) + lane;
+        per = kGroup;
+    } else if (lane == kGroup && s.block_map != nullptr) {
+        s_map = reinterpret_cast<const uint32_t *>(region(s.block_map, s.block_offset, 1));
+        d_map = reinterpret_cast<uint32_t *>(region(d.block_map, d.block_offset, 1));
+        per = 1;
+    } else if (lane == kGroup + 1 && s.weights != nullptr) {
+        s_map = reinterpret_cast<const uint32_t *>(region(s.weights, s.weight_offset, 1));
+        d_map = reinterpret_cast<uint32_t *>(region(d.weights, d.weight_offset, 1));
+        per = 1;
+    }
+    if (blockIdx.x == 0 && tid < 32) {  // the raw tail, by the first warp
+        if (lane == 0) d.visible[b] = kGroup * n + tail;
+        if (lane < tail && s_map != nullptr) d_map[int64_t(kGroup) * n] = __ldg(s_map + int64_t(kGroup) * G);
+        if (lane == kGroup + 1 && tail > 0 && s_map != nullptr) d_map[n] = __ldg(s_map + G);
+        if (s_raw != nullptr)
+            for (int e = lane; e < tail * F4; e += 32) d_raw[int64_t(kGroup * F4) * n + e] = __ldg(s_raw + int64_t(kGroup * F4) * G + e);
     }
     const int32_t *kept = a.kept + int64_t(b) * a.keep;
-    for (int i = int(blockIdx.x) * kMoveWarps + (tid >> 5); i < n; i += int(gridDim.x) * kMoveWarps) {
-        const int g = __ldg(kept + i);
-        const bool ok = g >= 0 && g < G;
-        if (!ok && lane == 0) set_error(a.err, QSA_DEVERR_ROW_RANGE);
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 raw[kRaw], pool = zero;
-        int map = -1;
-        float wt = 0.0f;
-        if (s.idx_keys != nullptr) {
-            const float4 *src = reinterpret_cast<const float4 *>(s.idx_keys + (__ldg(s.key_offset + b) + kGroup * int64_t(g)) * D);
+    const uint32_t none = lane == kGroup + 1 ? 0u : 0xffffffffu;  // of a bad position: weight 0, map entries -1
+    const int stride = int(gridDim.x) * kMoveWarps * kTake;
+    int i0 = (int(blockIdx.x) * kMoveWarps + (tid >> 5)) * kTake;
+    int next[kTake];
 #pragma unroll
-            for (int j = 0; j < kRaw; ++j) raw[j] = ok ? __ldg(src + lane + 32 * j) : zero;
-        }
-        if (s.pooled != nullptr && lane < F4 && ok)  // piece p of the new row: its place depends on the position
-            pool = __ldg(reinterpret_cast<const float4 *>(s.pooled + (__ldg(s.pool_offset + b) + g) * D) + (lane ^ (i & 7) ^ (g & 7)));
-        if (ok) {
-            if (s.slot_map != nullptr && lane < kGroup) map = __ldg(s.slot_map + __ldg(s.slot_offset + b) + kGroup * int64_t(g) + lane);
-            if (s.block_map != nullptr && lane == kGroup) map = __ldg(s.block_map + __ldg(s.block_offset + b) + g);
-            if (s.weights != nullptr && lane == kGroup + 1) wt = __ldg(s.weights + __ldg(s.weight_offset + b) + g);
-        }
-        if (s.idx_keys != nullptr) {
-            float4 *dst = reinterpret_cast<float4 *>(d.idx_keys + (__ldg(d.key_offset + b) + kGroup * int64_t(i)) * D);
+    for (int u = 0; u < kTake; ++u) next[u] = i0 + u < n ? __ldg(kept + i0 + u) : 0;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (; i0 < n; i0 += stride) {
+        float4 raw[kTake][kRaw], pool[kTake];
+        uint32_t map[kTake];
+        int g[kTake];
+        bool ok[kTake];
 #pragma unroll
-            for (int j = 0; j < kRaw; ++j) dst[lane + 32 * j] = raw[j];
+        for (int u = 0; u < kTake; ++u) {
+            g[u] = next[u];
+            ok[u] = i0 + u < n && g[u] >= 0 && g[u] < G;
+            if (i0 + u < n && !ok[u] && lane == 0) set_error(a.err, QSA_DEVERR_ROW_RANGE);
+            if (s_raw != nullptr) {
+#pragma unroll
+                for (int j = 0; j < kRaw; ++j) raw[u][j] = ok[u] ? __ldg(s_raw + int64_t(kGroup * F4) * g[u] + lane + 32 * j) : zero;
+            }
+            if (s_pool != nullptr && lane < F4)  // piece p of the new row: its place depends on the position
+                pool[u] = ok[u] ? __ldg(s_pool + int64_t(F4) * g[u] + (lane ^ ((i0 + u) & 7) ^ (g[u] & 7))) : zero;
+            if (s_map != nullptr) map[u] = ok[u] ? __ldg(s_map + int64_t(per) * g[u]) : none;
         }
-        if (s.pooled != nullptr && lane < F4)
-            reinterpret_cast<float4 *>(d.pooled + (__ldg(d.pool_offset + b) + i) * D)[lane] = pool;
-        if (s.slot_map != nullptr && lane < kGroup) d.slot_map[__ldg(d.slot_offset + b) + kGroup * int64_t(i) + lane] = map;
-        if (s.block_map != nullptr && lane == kGroup) d.block_map[__ldg(d.block_offset + b) + i] = map;
-        if (s.weights != nullptr && lane == kGroup + 1) d.weights[__ldg(d.weight_offset + b) + i] = wt;
+#pragma unroll
+        for (int u = 0; u < kTake; ++u) next[u] = i0 + stride + u < n ? __ldg(kept + i0 + stride + u) : 0;
+#pragma unroll
+        for (int u = 0; u < kTake; ++u) {
+            const int64_t i = i0 + u;
+            if (i >= n) break;
+            if (s_raw != nullptr) {
+#pragma unroll
+                for (int j = 0; j < kRaw; ++j) d_raw[int64_t(kGroup * F4) * i + lane + 32 * j] = raw[u][j];
+            }
+            if (s_pool != nullptr && lane < F4) d_pool[int64_t(F4) * i + lane] = pool[u];
+            if (s_map != nullptr) d_map[int64_t(per) * i] = map[u];
+        }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t s)
+template <int kRanks>
+static cudaError_t launch_select_t(const EvictSelectArgs &a, cudaStream_t s)
 {
-    if (a.batch == 0) return cudaSuccess;
     static bool attr_done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!attr_done[dev]) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
+        e = cudaFuncSetAttribute(evict_select_kernel<kRanks>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCached * 4);
         if (e != cudaSuccess) return e;
         attr_done[dev] = true;
     }
     const int groups = a.max_visible / kGroup;
-    const int nr = groups <= 4096 ? 1 : kCluster;
-    const int slice = ((groups + nr - 1) / nr + kPer - 1) / kPer * kPer;
+    const int slice = ((groups + kRanks - 1) / kRanks + kPer - 1) / kPer * kPer;
     const int cached = slice < kCached ? slice : kCached;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(nr), unsigned(a.batch));
+    cfg.gridDim = dim3(kRanks, unsigned(a.batch));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = size_t(cached) * 4;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(nr);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kRanks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cached);
+    cfg.numAttrs = kRanks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, evict_select_kernel<kRanks>, a, cached);
+}
+
+cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t s)
+{
+    if (a.batch == 0) return cudaSuccess;
+    return a.max_visible / kGroup <= kOneCta ? launch_select_t<1>(a, s) : launch_select_t<kCluster>(a, s);
 }
 
 cudaError_t launch_evict_compact(const EvictCompactArgs &a, int num_sms, cudaStream_t s)
 {
     if (a.batch == 0) return cudaSuccess;
     const int most = a.keep < a.max_visible / kGroup ? a.keep : a.max_visible / kGroup;
-    const int blocks = (most + kMoveWarps - 1) / kMoveWarps;
-    const int cap = 64 * num_sms;
+    const int per_cta = kMoveWarps * kTake;
+    const int blocks = (most + per_cta - 1) / per_cta, cap = kMoveCtas * num_sms / a.batch + 1;
     const dim3 grid(unsigned(blocks < 1 ? 1 : blocks < cap ? blocks : cap), unsigned(a.batch));
-    if (a.idx_dim == 64) evict_compact_kernel<64><<<grid, kMoveThreads, 0, s>>>(a);
-    else if (a.idx_dim == 32) evict_compact_kernel<32><<<grid, kMoveThreads, 0, s>>>(a);
-    else return cudaErrorInvalidValue;
-    return cudaGetLastError();
+    if (a.idx_dim == 64) return launch_kernel(evict_compact_kernel<64>, grid, dim3(kMoveThreads), 0, s, true, a);
+    if (a.idx_dim == 32) return launch_kernel(evict_compact_kernel<32>, grid, dim3(kMoveThreads), 0, s, true, a);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace qsa
