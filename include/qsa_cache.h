@@ -6,7 +6,9 @@
  * buffer, asynchronous on `stream`, host-detectable errors before anything is
  * enqueued, device-detected errors in the workspace's sticky error word,
  * results that depend neither on the rest of the batch nor on the number of
- * SMs, calls that share a workspace must not overlap on the GPU).
+ * SMs, calls that share a workspace must not overlap on the GPU).  Kernels are
+ * launched programmatically, as qsa_score_pooled's is: each waits for the kernel
+ * before it on `stream` before it reads or writes anything, so stream order holds.
  *
  * The notes that define the method have no counterpart to this header.  It
  * keeps to their units: the four-token group that is scored, selected and
@@ -73,7 +75,7 @@ qsa_status qsa_code_groups(const qsa_dims *dims, const qsa_inputs *in, const qsa
 /* Workspace of the calls below that attend over a coded cache (0 if the dims
  * are invalid): qsa_workspace_size(dims) when both flags are 0, followed by
  *   whole_history: the attention's partial states, n_q*(d+2) floats per run of
- *     a row and query, at most 514 runs;
+ *     a row and query, at most 513 runs;
  *   with_weights: n_q * (1.25 * groups of a row + 2) + 2 floats per query, groups =
  *     max_visible/4 for whole histories, else budget_groups.
  * Linear in the history, never queries x keys of other queries.  A workspace

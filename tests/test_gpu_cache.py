@@ -193,6 +193,25 @@ def test_attention_over_whole_histories(fmt, q_heads, kv, d):
     assert abs((got - h.weights0).sum() - q_heads * np.count_nonzero(h.visible)) < 1e-3 * q_heads
 
 
+@pytest.mark.parametrize("fmt,q_heads", [(ch.E4M3, 3), (ch.INT8, 12)])
+def test_attention_over_long_histories(fmt, q_heads):
+    """Rows on both sides of each change of the run length, whose runs take several
+    segments, beside short ones."""
+    need_gpu()
+    h = ch.History([4 * 4097 + 1, 5, 4 * 4096, 4 * 65537 + 2, 4 * 131073 + 3], q_heads=q_heads, kv_heads=1, head_dim=64, fmt=fmt,
+                   seed=27)
+    t = ch.device(h, whole=True, weights=True)
+    ch.fill_cache(h, t)
+    ref, share, tol, rel = ch.attention(h)
+    # (more runs per slice and more steps per warp than the bound of shorter rows counts: 512/8 + 128 additions)
+    vmax = max(float(np.abs(h.v).max()), 1.0) * 1.1
+    _close(h, _attend(t, weights=True), ref, tol + vmax * 192 * 2.0 ** -24)
+    _ok(t)
+    w, wt = ch.add_weights(h, share, [r + 192 * 2.0 ** -24 for r in rel])
+    got = t["weights"].cpu().numpy().astype(np.float64)
+    assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()
+
+
 @pytest.mark.parametrize("budget", [512, 32, 5, 1])
 @pytest.mark.parametrize("fmt,q_heads,kv,d", [(ch.E4M3, 16, 2, 128), (ch.INT8, 8, 2, 64), (ch.INT8, 16, 1, 128), (ch.E4M3, 3, 3, 64)])
 def test_attention_over_selected_rows(budget, fmt, q_heads, kv, d):
@@ -436,3 +455,93 @@ def test_a_captured_call_replays_on_new_inputs_and_another_stream():
         _attend(t2)
         _ok(t2)
     _ok(t)
+
+
+def test_device_batch_runs_the_coded_cache():
+    """DeviceBatch: coding, the whole path and the observation of whole histories,
+    independent ones and a shared one."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    from top_group_sparse_gb300 import workloads as wl
+    for vis, history in (([300, 2053, 0, 7], "independent"), ([997, 998, 1001, 1003], "shared")):
+        w = wl.make_workload("coded", vis, idx_heads=4, idx_dim=32, q_heads=8, kv_heads=2, head_dim=64, seed=51, slots="paged16",
+                             history=history, budget=33)
+        db = qsa.DeviceBatch(w)
+        db.make_coded_cache(qsa.QSA_CODE_INT8)
+        db.code_all()
+        db.decode_coded(weigh=True)
+        assert qsa.qsa_check_errors(db.coded_ws)[1] == 0
+        h = ch.History(vis, q_heads=8, kv_heads=2, head_dim=64, fmt=ch.INT8, seed=52, shared=history == "shared")
+        h.q, h.k, h.v = w.q, w.k_cache[w.slot_map], w.v_cache[w.slot_map]
+        h.weights0 = np.zeros(max(h.n_weights, 1), np.float32)
+        assert np.array_equal(db.weight_offset.cpu().numpy(), h.weight_offset)
+        rows = [db.ids[b, :int(db.n_ids[b])].cpu().numpy() for b in range(4)]
+        ref, share, tol, rel = ch.attention(h, rows)
+        _close(h, db.out, ref, tol)
+        wt, at = ch.add_weights(h, share, rel)
+        assert (np.abs(db.weights.cpu().numpy() - wt) <= at).all()
+        db.attend_coded()
+        _close(h, db.out, ref, tol)
+        db.weights.zero_()
+        db.attend_coded(whole=True, weigh=True)
+        ref, share, tol, rel = ch.attention(h)
+        _close(h, db.out, ref, tol)
+        wt, at = ch.add_weights(h, share, rel)
+        assert (np.abs(db.weights.cpu().numpy() - wt) <= at).all()
+        assert qsa.qsa_check_errors(db.coded_ws)[1] == 0
+
+
+def test_caches_beyond_two_to_the_31():
+    """Blocks whose codes start beyond byte 2^31 and slots whose rows start beyond
+    element 2^31: coded, and attended to, as anywhere else."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    h = ch.History([70, 515], q_heads=16, kv_heads=2, head_dim=128, fmt=ch.INT8, seed=61)
+    t = ch.device(h, whole=True)
+    high_slot, high_block = 2 ** 31 // 256 + 5, 2 ** 31 // 2048 + 7
+    num_slots, num_blocks = high_slot + h.num_slots, high_block + h.num_blocks
+    k = torch.zeros(num_slots, 2, 128, device="cuda")
+    v = torch.zeros(num_slots, 2, 128, device="cuda")
+    k[high_slot:].copy_(t["k_cache"])
+    v[high_slot:].copy_(t["v_cache"])
+    codes = torch.zeros(num_blocks, 2, 1024, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(num_blocks, 2, 2, device="cuda")
+    t["slot_map"] += high_slot
+    t["block_map"] += high_block
+    inp = qsa.QsaInputs(visible=t["visible"].data_ptr(), q=t["q"].data_ptr(), k_cache=k.data_ptr(), v_cache=v.data_ptr(),
+                        num_slots=num_slots, slot_map=t["slot_map"].data_ptr(), slot_offset=t["token_offset"].data_ptr())
+    cache = qsa.QsaCodedCache.of(codes, scales, t["block_map"], t["group_offset"], h.fmt)
+    qsa.qsa_code_groups(t["dims"], inp, cache, t["lo"], t["hi"], t["most"], t["ws"])
+    qsa.qsa_attend_coded(t["dims"], inp, cache, None, None, t["out"], t["ws"])
+    _ok(t)
+    assert (codes[:high_block] == 0).all()
+    ref, _, tol, _ = ch.attention(h)
+    _close(h, t["out"], ref, tol)
+
+
+def test_two_streams_at_once():
+    """Two batches on two streams, each with a workspace of its own, many times over:
+    both give what they give alone."""
+    torch = need_gpu()
+    hs = [ch.History([9001, 515, 0, 4099], q_heads=16, kv_heads=2, head_dim=128, fmt=ch.E4M3, seed=71),
+          ch.History([3, 2048, 7001], q_heads=8, kv_heads=8, head_dim=64, fmt=ch.INT8, seed=72)]
+    ts = [ch.device(h, whole=True, weights=True) for h in hs]
+    alone = []
+    for h, t in zip(hs, ts):
+        ch.fill_cache(h, t)
+        _attend(t, weights=True)
+        alone.append((t["out"].clone(), t["weights"].clone()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ts]
+    outs = [[], []]
+    for _ in range(20):
+        for i, (h, t, s) in enumerate(zip(hs, ts, streams)):
+            with torch.cuda.stream(s):
+                t["weights"].copy_(torch.from_numpy(h.weights0).pin_memory(), non_blocking=True)
+                _attend(t, weights=True)
+                outs[i].append((t["out"].clone(), t["weights"].clone()))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, w in outs[i]:
+            assert torch.equal(out, alone[i][0]) and torch.equal(w, alone[i][1])
+        _ok(ts[i])

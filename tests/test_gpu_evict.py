@@ -178,6 +178,41 @@ def test_the_move_equals_the_definition(idx_dim, keep):
             assert np.array_equal(d[k].cpu().numpy(), ref), (k, left_out)
 
 
+def test_a_captured_eviction_replays_on_new_weights():
+    """Selection and move captured once; replayed, they go by the weights of the day."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    visible, keep = [403, 40000], 50
+    src = _history(visible, 64, 5)
+    dims = qsa.make_dims(2, 8, 64, 16, 2, 128, max_visible=max(visible))
+    ws = torch.zeros(qsa.qsa_workspace_size(dims), dtype=torch.uint8, device="cuda")
+    dst = _history([4 * keep + t % 4 for t in visible], 64, 6, fill=-7)
+    s = {k: torch.from_numpy(v).cuda() for k, v in src.items()}
+    d = {k: torch.from_numpy(v.copy()).cuda() for k, v in dst.items()}
+    kept = torch.full((2, keep), -1, dtype=torch.int32, device="cuda")
+    n_kept = torch.zeros(2, dtype=torch.int32, device="cuda")
+
+    def run():
+        qsa.qsa_evict_select(dims, s["visible"], s["weights"], s["weight_offset"], keep, 1, 3, kept, n_kept, ws)
+        qsa.qsa_evict_compact(dims, keep, kept, n_kept, qsa.QsaHistory.of(**s), qsa.QsaHistory.of(**d), ws)
+
+    run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for seed in (7, 8):
+        src["weights"] = np.random.RandomState(seed).rand(len(src["weights"])).astype(np.float32)
+        s["weights"].copy_(torch.from_numpy(src["weights"]))
+        g.replay()
+        assert qsa.qsa_check_errors(ws)[1] == 0
+        want = ch.evict(visible, src["weights"], src["weight_offset"], keep, 1, 3)
+        assert np.array_equal(kept.cpu().numpy(), np.array(want))
+        moved = _moved(src, dst, want, 64)
+        for k in d:
+            assert np.array_equal(d[k].cpu().numpy(), moved[k]), k
+
+
 def test_the_move_flags_what_is_out_of_range():
     torch = need_gpu()
     from top_group_sparse_gb300 import qsa

@@ -9,14 +9,15 @@
 //
 // An 8-bit code is exact in a 16-bit float, so both products run on the tensor
 // cores with operands that lose nothing: q and the weights w_t = p_t sV_g enter
-// as hi + lo, two 16-bit floats of 11 bits each, scaled by a power of two so
-// that the larger of them sits near 2^14 (both halves stay clear of the 16-bit
-// subnormals).  The matrix instruction m16n8k16 has 16 rows; with at most 8
-// query heads per KV head, rows 0-7 hold the hi parts and rows 8-15 the lo
-// parts of the same heads, so one instruction does both and its two result rows
-// h and h+8, which the same lane holds, add up to the product.  (9 to 16 heads:
-// rows are heads, and the lo parts follow the hi parts into the same sum.)  Every instruction chain starts from zero and its result is added
-// to the binary32 running sums by ordinary additions, which round to nearest.
+// as hi + lo, two 16-bit floats of 11 bits each, scaled by a power of two that
+// keeps both halves clear of the 16-bit subnormals where they matter.  The
+// matrix instruction m16n8k16 has 16 rows; with at most 8 query heads per KV
+// head, rows 0-7 hold the hi parts and rows 8-15 the lo parts of the same heads,
+// so one instruction does both and its two result rows h and h+8, which the same
+// lane holds, add up to the product.  (9 to 16 heads: rows are heads, and the lo
+// parts follow the hi parts into the same sum.)  The tensor core's own sums may
+// truncate, so a chain covers 16 tokens, or d dims, and starts from zero; its
+// result goes into the binary32 running sums by additions that round to nearest.
 //
 // Layout.  A warp step is 4 groups (16 tokens).  For the first product tile t
 // holds tokens 2t, 2t+1 of the 4 groups (column n: group n/2, token 2t + n%2),
@@ -27,7 +28,24 @@
 // one word of the V layout.  A block of codes sits in shared memory with 32
 // bytes behind it: the 16-byte reads of both products are free of conflicts.
 //
-// Bound by memory: 8*d + 8 bytes per (group, KV head), read once.
+// Data movement.  A CTA of four warps takes one run of a row; each warp streams
+// its own steps through a ring of two (16-byte asynchronous copies, a step ahead
+// of its arithmetic), so there is no block barrier in the loop.  Four CTAs per SM
+// (128 registers) cover one another's starts -- the row, its blocks, their scales
+// and the query are three dependent loads -- and ends.
+//
+// Bound: 8*d + 8 bytes per (group, KV head), read once.  8 histories of 262,144
+// tokens (16 / 2 heads x 128, e4m3, 1.08 GB): 177 us of this kernel, 6.1 TB/s, the
+// tensor pipe 25-30 % and the issue slots about half busy; with the blocks in
+// order instead of permuted 7 % less, the rest of the distance to the copy rate
+// (6.77 TB/s) being starts and ends.  Rows of a few thousand tokens and selected
+// rows (512 groups: 5.4 us for 8 queries) are bound by a CTA's start and end.
+// Tried and not kept: a ring of three (189 us), copies by the bulk engine (its
+// operands are uniform, so four lanes' copies are issued one after the other:
+// 60 more instructions a step, 188 us), resident CTAs that take several runs with
+// the next run's addresses loaded ahead (199-207 us: a fixed share of the runs
+// waits for the slowest SM), two runs of selected rows per CTA, five CTAs per SM
+// with q read from shared memory at each step (191 us).
 #include <cuda_fp16.h>
 
 #include "cache_internal.cuh"
@@ -38,7 +56,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStepGroups = 4;                  // groups per warp step
-constexpr int kRing = 2;                        // steps in flight per warp
+constexpr int kRing = 2;                        // a warp's steps in shared memory: one in use, one on its way
 constexpr int kSegGroups = 128;                 // groups resolved at a time
 constexpr int kBlkPad = 32;                     // bytes behind a block in shared memory
 

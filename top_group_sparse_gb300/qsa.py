@@ -707,6 +707,64 @@ class DeviceBatch:
         return qsa_decode_pooled(self.dims, self.inputs, self.pooled, self.pool_offset, self.ids,
                                  self.n_ids, self.out, self.ws, stream)
 
+    # ---- a K/V cache in 8 bits ------------------------------------------------
+    def make_coded_cache(self, fmt=QSA_CODE_E4M3):
+        """Allocates the coded cache: one block per complete group of each distinct
+        history (in order), its accumulated weights (one per group and one for an
+        incomplete one) and a workspace that serves every call on this batch."""
+        import torch
+        ko = self.key_offset.cpu().numpy()
+        T = self.visible.cpu().numpy()
+        block, weight, blocks, weights, owner = {}, {}, 0, 0, {}
+        for b, k in enumerate(ko.tolist()):
+            if k not in owner or T[b] > T[owner[k]]:
+                owner[k] = b
+        for k in sorted(owner):
+            block[k], weight[k] = blocks, weights
+            blocks += int(T[owner[k]]) // 4
+            weights += -(-int(T[owner[k]]) // 4)
+        dev, w = self.q.device, self.w
+
+        def put(rows):
+            return torch.from_numpy(np.array([rows[k] for k in ko.tolist()], np.int64)).to(dev)
+
+        self.block_offset, self.weight_offset = put(block), put(weight)
+        self.block_map = torch.arange(max(blocks, 1), dtype=torch.int32, device=dev)
+        self.codes = torch.zeros((max(blocks, 1), w.kv_heads, 8 * w.head_dim), dtype=torch.uint8, device=dev)
+        self.scales = torch.zeros((max(blocks, 1), w.kv_heads, 2), dtype=torch.float32, device=dev)
+        self.weights = torch.zeros(max(weights, 1), dtype=torch.float32, device=dev)
+        self.coded = QsaCodedCache.of(self.codes, self.scales, self.block_map, self.block_offset, fmt)
+        self.coded_ws = torch.zeros(qsa_coded_workspace_size(self.dims, True, True), dtype=torch.uint8, device=dev)
+        self._code_owner = np.array([owner[k] == b for b, k in enumerate(ko.tolist())])
+        return self.coded
+
+    def code(self, group_begin, group_end, stream=None):
+        """Codes groups [group_begin[b], group_end[b]) of every query (host arrays)."""
+        import torch
+        gb, ge = np.asarray(group_begin, np.int32), np.asarray(group_end, np.int32)
+        dev = self.q.device
+        self._code_args = (torch.from_numpy(gb).to(dev), torch.from_numpy(ge).to(dev))
+        return qsa_code_groups(self.dims, self.inputs, self.coded, self._code_args[0], self._code_args[1],
+                               max(int((ge - gb).max(initial=0)), 0), self.coded_ws, stream)
+
+    def code_all(self, stream=None):
+        """Codes every complete group of every history (once per history)."""
+        ge = np.where(self._code_owner, self.visible.cpu().numpy() // 4, 0).astype(np.int32)
+        return self.code(np.zeros_like(ge), ge, stream)
+
+    def attend_coded(self, whole=False, weigh=False, stream=None):
+        """Attention over the coded cache: the rows in ids / n_ids, or the whole histories."""
+        return qsa_attend_coded(self.dims, self.inputs, self.coded, None if whole else self.ids,
+                                None if whole else self.n_ids, self.out, self.coded_ws,
+                                weights=self.weights if weigh else None,
+                                weight_offset=self.weight_offset if weigh else None, stream=stream)
+
+    def decode_coded(self, weigh=False, stream=None):
+        """The whole path over the coded cache (scored from the raw index keys)."""
+        return qsa_decode_coded(self.dims, self.inputs, self.coded, self.ids, self.n_ids, self.out, self.coded_ws,
+                                weights=self.weights if weigh else None,
+                                weight_offset=self.weight_offset if weigh else None, stream=stream)
+
     # ---- queries over one shared history ------------------------------------
     def score_shared(self, stream=None):
         return qsa_score_groups_shared(self.dims, self.inputs, self.scores, self.ws, stream)
