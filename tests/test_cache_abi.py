@@ -66,8 +66,8 @@ def test_workspace_closed_forms(lib):
     base = qsa.qsa_workspace_size(d)
     assert qsa.qsa_coded_workspace_size(d, False, False) == base
     heads = 2 * 16
-    # 1,024 groups: 32 runs of 32, and the tail's
-    part = 2 * up(heads * 33 * 4) + up(heads * 33 * 128 * 4)
+    # 1,024 groups: 16 runs of 64, and the tail's
+    part = 2 * up(heads * 17 * 4) + up(heads * 17 * 128 * 4)
     assert qsa.qsa_coded_workspace_size(d, True, False) == base + part
     mass = up(heads * 1024 * 4) + up(heads * 256 * 4) + up(heads * 8) + 2 * up(2 * 4)
     assert qsa.qsa_coded_workspace_size(d, True, True) == base + part + mass

@@ -14,19 +14,20 @@ namespace qsa {
 // head only, so the bits of an output do not depend on the batch.  Shorter runs
 // spread a row over more SMs, longer ones pay less for a CTA's start and for the
 // partial states (n_q/n_kv * (d+2) * 4 bytes per run against 8*d per group).
-// Measured, whole histories of 32 ragged rows of up to 16,384 groups (8 heads):
-// runs of 128 take 95 us, of 256 84 us; 4 rows of 10,000 groups with 16 heads:
-// 21 and 27 us; 12 rows of up to 2,250 groups: runs of 64 16 us, of 128 18 us.
-// Selected rows (at most 512 groups), 256 queries: runs of 32 85 us, of 64 68 us;
-// 8 queries: 6.1 us both.  Beyond 65,536 groups the length doubles so that a row has
-// at most 512 runs.
+// Measured (this kernel alone, us): 64 rows of 1,024 groups, 8 heads of their own x
+// 64: runs of 32 84, of 64 63, of 128 55; one such row 4.2, 4.8, 6.7.  64 rows of 4,096
+// groups, 16 / 2 heads x 128: runs of 64 107, of 128 96; 32 ragged rows of up to
+// 16,384 groups: runs of 128 95, of 256 84.  4 rows of 10,000 groups with 16 heads on
+// one: 128 19, 256 27.  Selected rows (at most 512 groups): 128 queries 45, 35, 31 with
+// runs of 32, 64, 128; 8 queries 5.1, 5.3, 7.2.  Beyond 131,072 groups the length
+// doubles so that a row has at most 512 runs.
 constexpr int kCodedRunRows = 64;
 
 __host__ __device__ inline int coded_run_groups(int groups, bool whole, int heads_per_kv)
 {
     if (!whole) return kCodedRunRows;
-    if (groups <= 1024) return 32;
-    if (groups <= 4096) return 64;
+    if (groups <= 1024) return 64;
+    if (groups <= 4096) return 128;
     int r = heads_per_kv > 8 ? 128 : 256;
     while ((groups + r - 1) / r > 512) r *= 2;
     return r;
