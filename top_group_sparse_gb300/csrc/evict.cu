@@ -35,8 +35,8 @@ constexpr int kOneCta = 4096;               // histories of up to so many groups
 
 struct SelectSmem {
     alignas(16) uint32_t hist[3][kBins];    // one per pass: a pass needs no barrier behind the others' reads
-    uint32_t warp_sum[2][kWarps];
-    uint32_t bin, rest;
+    uint32_t warp_sum[2][kWarps];           // by turns: a scan needs one barrier
+    uint32_t bin, rest, equal;
 };
 
 __device__ __forceinline__ uint32_t weight_key(float w)
@@ -44,39 +44,28 @@ __device__ __forceinline__ uint32_t weight_key(float w)
     return w != w ? 0u : order_key(w);
 }
 
-// Sum over the block of (x, y), and the exclusive prefix of each thread.
-__device__ __forceinline__ void block_scan2(SelectSmem &sm, uint32_t &x, uint32_t &y, uint32_t &tx, uint32_t &ty)
+// The exclusive prefix of x over the block, and the sum; one barrier.
+__device__ __forceinline__ uint32_t block_scan(SelectSmem &sm, int &turn, uint32_t x, uint32_t &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t x0 = x, y0 = y;
+    uint32_t incl = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-            x += u;
-            y += v;
-        }
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
     }
+    if (lane == 31) sm.warp_sum[turn][warp] = incl;
     __syncthreads();
-    if (lane == 31) {
-        sm.warp_sum[0][warp] = x;
-        sm.warp_sum[1][warp] = y;
-    }
-    __syncthreads();
-    uint32_t px = 0, py = 0;
-    tx = ty = 0;
+    uint32_t sums = lane < kWarps ? sm.warp_sum[turn][lane] : 0u;
+    turn ^= 1;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const uint32_t a = sm.warp_sum[0][w], b = sm.warp_sum[1][w];
-        if (w < warp) {
-            px += a;
-            py += b;
-        }
-        tx += a;
-        ty += b;
+    for (int o = 1; o < kWarps; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xffffffffu, sums, o);
+        if (lane >= o) sums += u;
     }
-    x += px - x0;
-    y += py - y0;
+    total = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+    const uint32_t before = __shfl_sync(0xffffffffu, sums, warp > 0 ? warp - 1 : 0);
+    return (warp > 0 ? before : 0u) + incl - x;
 }
 
 template <int kRanks>
@@ -124,8 +113,9 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
     // above and equal to K in the slices before this one ----------------------------------
     uint32_t K = 0xffffffffu, ties = 0;  // (no key is that large: nothing is kept)
     uint32_t base_gt = 0, base_eq = 0;
+    int turn = 0;
     if (need > 0) {
-        uint32_t rest = need, prefix = 0;
+        uint32_t rest = need, prefix = 0, my_gt = 0;
         int shift = 21, bits = 11;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
@@ -162,23 +152,19 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
                     if (r < rank) before[j] += x[j];
                 }
             }
-            uint32_t above = (c[0] + c[1]) + (c[2] + c[3]), none = 0, total, unused;
-            block_scan2(sm, above, none, total, unused);  // above: keys in the bins above this thread's
-            uint32_t gt = 0, eq = 0;
+            uint32_t total;
+            uint32_t above = block_scan(sm, turn, (c[0] + c[1]) + (c[2] + c[3]), total);  // keys in the bins above this thread's
 #pragma unroll
             for (int j = 0; j < kMine; ++j) {
-                if (above + c[j] < rest) gt += before[j];  // a bin above K's
-                if (above < rest && rest <= above + c[j]) {  // K's bin: exactly one bin of one thread
+                if (above + c[j] < rest) my_gt += before[j];  // a bin above K's
+                if (above < rest && rest <= above + c[j]) {   // K's bin: exactly one bin of one thread
                     sm.bin = uint32_t(first_bin + kMine - 1 - j);
                     sm.rest = rest - above;
-                    if (pass == 2) eq = before[j];
+                    sm.equal = before[j];
                 }
                 above += c[j];
             }
-            uint32_t tg, te;
-            block_scan2(sm, gt, eq, tg, te);  // (also: sm.bin is there)
-            base_gt += tg;
-            base_eq = te;
+            __syncthreads();
             prefix |= sm.bin << shift;
             rest = sm.rest;
             bits = pass == 1 ? 10 : 11;
@@ -186,6 +172,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
         }
         K = prefix;
         ties = rest;
+        base_eq = sm.equal;
+        if constexpr (kRanks > 1) (void)block_scan(sm, turn, my_gt, base_gt);
     }
     // no CTA leaves while another may read its counts: this one has read the others'
     if constexpr (kRanks > 1) cluster.barrier_arrive();
@@ -193,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
     // ---- emission in ascending position ------------------------------------------------
     for (int i0 = 0; i0 < sn; i0 += kThreads * kPer) {
         const int first = i0 + tid * kPer;
-        uint32_t k[kPer], gt = 0, eq = 0, tg, te;
+        uint32_t k[kPer], gt = 0, eq = 0, total;
         if (in_smem) {  // (16-byte reads; what is behind the slice is not used)
 #pragma unroll
             for (int j = 0; j < kPer; j += 4) {
@@ -211,21 +199,22 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
                 eq += k[j] == K;
             }
         }
-        block_scan2(sm, gt, eq, tg, te);
-        uint32_t pg = base_gt + gt, pe = base_eq + eq;
+        static_assert(kThreads * kPer < 65536, "both counts of a turn in one word");
+        const uint32_t before = block_scan(sm, turn, gt | (eq << 16), total);
+        uint32_t pg = base_gt + (before & 0xffffu), pe = base_eq + (before >> 16);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             if (first + j >= sn) break;
             const int p = s0 + first + j;  // position - lo
-            const uint32_t before = pg + min(pe, ties);
+            const uint32_t at = pg + min(pe, ties);  // kept before it
             const bool keep = k[j] > K || (k[j] == K && pe < ties);
-            if (keep) kept[a.sink + before] = lo + p;
-            else if (evicted != nullptr) evicted[uint32_t(p) - before] = lo + p;
+            if (keep) kept[a.sink + at] = lo + p;
+            else if (evicted != nullptr) evicted[uint32_t(p) - at] = lo + p;
             pg += k[j] > K;
             pe += k[j] == K;
         }
-        base_gt += tg;
-        base_eq += te;
+        base_gt += total & 0xffffu;
+        base_eq += total >> 16;
     }
     if (rank == 0) {
         for (int g = tid; g < a.sink; g += kThreads) kept[g] = g;
