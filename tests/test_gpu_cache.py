@@ -285,6 +285,74 @@ def test_weights_of_several_shared_histories_in_one_batch(whole):
     assert torch.equal(t["weights"], again)
 
 
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("sharers", [2, 3, 8, 9, 12, 530])
+def test_a_shared_sum_does_not_depend_on_the_rest_of_the_batch(whole, sharers):
+    """Queries that share accumulators add the same bits alone and among queries of
+    other histories (each with accumulators of its own, or shared by two)."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    r = np.random.RandomState(27)
+    B = 3 * sharers
+    mine = np.sort(r.permutation(B)[:sharers])
+    h = ch.History([int(t) for t in r.randint(1, 400, B)], q_heads=4, kv_heads=1, head_dim=64, fmt=ch.E4M3, seed=28)
+    room = 100
+    pick = 1 + np.arange(B) // 2
+    pick[mine] = 0
+    h.weight_offset = (pick * room).astype(np.int64)
+    h.n_weights = (2 + B) * room
+    h.weights0 = r.rand(h.n_weights).astype(np.float32)
+    budget = 40
+    t = ch.device(h, budget=budget, whole=whole, weights=True, max_visible=400)
+    ch.fill_cache(h, t)
+    rows = None if whole else ch.some_rows(h, budget, 29)
+    ids, n = (None, None) if whole else ch.rows_to_device(rows, budget)
+    _, share, _, rel = ch.attention(h, rows)
+    _attend(t, ids, n, weights=True)
+    _ok(t)
+    w, wt = ch.add_weights(h, share, rel)
+    assert (np.abs(t["weights"].cpu().numpy() - w) <= wt).all()
+    among = t["weights"][:room].clone()
+    sel = torch.from_numpy(mine).cuda()
+    one = {k: t[k][sel].contiguous() for k in ("visible", "q", "token_offset", "group_offset", "weight_offset")}
+    dims = qsa.make_dims(sharers, 8, 64, 4, 1, 64, budget_groups=budget, max_visible=400, scale=h.scale)
+    ws = torch.zeros(qsa.qsa_coded_workspace_size(dims, whole, True), dtype=torch.uint8, device="cuda")
+    inp = qsa.QsaInputs(visible=one["visible"].data_ptr(), q=one["q"].data_ptr(), k_cache=t["k_cache"].data_ptr(),
+                        v_cache=t["v_cache"].data_ptr(), num_slots=h.num_slots, slot_map=t["slot_map"].data_ptr(),
+                        slot_offset=one["token_offset"].data_ptr())
+    cache = qsa.QsaCodedCache.of(t["codes"], t["scales"], t["block_map"], one["group_offset"], h.fmt)
+    alone = torch.from_numpy(h.weights0).cuda()
+    out = torch.empty(sharers, 4, 64, device="cuda")
+    some = (None, None) if whole else (ids[sel].contiguous(), n[sel].contiguous())
+    qsa.qsa_attend_coded(dims, inp, cache, *some, out, ws, weights=alone, weight_offset=one["weight_offset"])
+    assert torch.equal(alone[:room], among)
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_weights_of_many_shared_histories(whole):
+    """300 histories of two queries each, interleaved: more units of work than CTAs."""
+    torch = need_gpu()
+    r = np.random.RandomState(30)
+    B, room = 600, 260
+    h = ch.History([int(t) for t in r.randint(800, 1030, B)], q_heads=2, kv_heads=1, head_dim=64, fmt=ch.INT8, seed=31)
+    h.weight_offset = (np.arange(B) % 300 * room).astype(np.int64)
+    h.n_weights = 300 * room
+    h.weights0 = r.rand(h.n_weights).astype(np.float32)
+    t = ch.device(h, budget=20, whole=whole, weights=True)
+    ch.fill_cache(h, t)
+    rows = None if whole else ch.some_rows(h, 20, 32)
+    ids, n = (None, None) if whole else ch.rows_to_device(rows, 20)
+    _, share, _, rel = ch.attention(h, rows)
+    _attend(t, ids, n, weights=True)
+    _ok(t)
+    w, wt = ch.add_weights(h, share, rel)
+    assert (np.abs(t["weights"].cpu().numpy() - w) <= wt).all()
+    again = t["weights"].clone()
+    t["weights"].copy_(torch.from_numpy(h.weights0))
+    _attend(t, ids, n, weights=True)
+    assert torch.equal(t["weights"], again)
+
+
 def test_an_output_does_not_depend_on_the_batch_or_the_workspace():
     """Each query alone, in a workspace made for its own length, gives the bits it
     gives in the batch, call after call."""
