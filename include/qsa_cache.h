@@ -99,7 +99,8 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * weights (NULL: none): accumulated attention.  weights[weight_offset[b] + g]
  * += sum over heads h and over the row's tokens t of group g = t/4 of
  * softmax(x)_t, the incomplete last group (g = visible[b]/4) included, so one
- * query adds n_q in all.  Queries with the same weight_offset share a history:
+ * query adds n_q in all; a row with a score that is NaN makes its groups' weights
+ * NaN.  Queries with the same weight_offset share a history:
  * their shares are added in a fixed order, so the sum has one value (the rows of
  * different offsets must not overlap).
  *

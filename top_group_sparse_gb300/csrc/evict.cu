@@ -306,8 +306,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Evict
 #pragma unroll
                 for (int j = 0; j < kRaw; ++j) raw[u][j] = ok[u] ? __ldg(s_raw + int64_t(kGroup * F4) * g[u] + lane + 32 * j) : zero;
             }
-            if (s_pool != nullptr && lane < F4)  // piece p of the new row: its place depends on the position
-                pool[u] = ok[u] ? __ldg(s_pool + int64_t(F4) * g[u] + (lane ^ ((i0 + u) & 7) ^ (g[u] & 7))) : zero;
+            // piece p of the new row: its place depends on the position.  (Through L2: the append
+            // of pooled keys lets its successor start before it has written.)
+            if (s_pool != nullptr && lane < F4)
+                pool[u] = ok[u] ? __ldcg(s_pool + int64_t(F4) * g[u] + (lane ^ ((i0 + u) & 7) ^ (g[u] & 7))) : zero;
             if (s_map != nullptr) map[u] = ok[u] ? __ldg(s_map + int64_t(per) * g[u]) : none;
         }
 #pragma unroll
