@@ -559,6 +559,39 @@ def test_device_batch_runs_the_coded_cache():
         assert qsa.qsa_check_errors(db.coded_ws)[1] == 0
 
 
+def test_device_batch_codes_on_the_stream_it_is_given():
+    """Calls one after the other on a side stream that is far behind, with other work taking
+    and filling memory meanwhile: each still finds its own ranges.  Ranges of another
+    length than the batch are refused."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    from top_group_sparse_gb300 import workloads as wl
+    w = wl.make_workload("coded", [301, 2053, 1000, 7], idx_heads=4, idx_dim=32, q_heads=8, kv_heads=2, head_dim=64, seed=53,
+                         slots="paged16", budget=33)
+    db = qsa.DeviceBatch(w)
+    db.make_coded_cache()
+    db.code_all()
+    torch.cuda.synchronize()
+    codes, scales = db.codes.clone(), db.scales.clone()
+    db.codes.zero_()
+    db.scales.zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    G = np.array(w.visible) // 4
+    cuts = [G * i // 5 for i in range(6)]
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    for i in range(5):
+        db.code(cuts[i], cuts[i + 1], stream=side.cuda_stream if i % 2 else side)
+        junk = [torch.full((4,), -1, dtype=torch.int32, device="cuda") for _ in range(64)]
+    torch.cuda.synchronize()
+    assert len(junk) == 64 and qsa.qsa_check_errors(db.coded_ws)[1] == 0
+    assert torch.equal(db.codes, codes) and torch.equal(db.scales, scales)
+    for bad in ([0, 0, 0], [[0, 0, 0, 0]], 0):
+        with pytest.raises(ValueError):
+            db.code(bad, bad)
+
+
 def test_caches_beyond_two_to_the_31():
     """Blocks whose codes start beyond byte 2^31 and slots whose rows start beyond
     element 2^31: coded, and attended to, as anywhere else."""

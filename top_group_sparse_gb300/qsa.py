@@ -739,13 +739,18 @@ class DeviceBatch:
         return self.coded
 
     def code(self, group_begin, group_end, stream=None):
-        """Codes groups [group_begin[b], group_end[b]) of every query (host arrays)."""
+        """Codes groups [group_begin[b], group_end[b]) of every query (host arrays, copied on `stream`:
+        not for a capture, where qsa_code_groups takes device arrays)."""
         import torch
         gb, ge = np.asarray(group_begin, np.int32), np.asarray(group_end, np.int32)
-        dev = self.q.device
-        self._code_args = (torch.from_numpy(gb).to(dev), torch.from_numpy(ge).to(dev))
-        return qsa_code_groups(self.dims, self.inputs, self.coded, self._code_args[0], self._code_args[1],
-                               max(int((ge - gb).max(initial=0)), 0), self.coded_ws, stream)
+        if gb.shape != (self.dims.batch,) or ge.shape != gb.shape:
+            raise ValueError(f"group_begin and group_end have one entry per query ({self.dims.batch})")
+        handle = _stream(stream)
+        on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        with torch.cuda.stream(on):  # their memory is that stream's, until the next call there
+            args = torch.from_numpy(np.stack([gb, ge])).to(self.q.device)
+            return qsa_code_groups(self.dims, self.inputs, self.coded, args[0], args[1],
+                                   max(int((ge - gb).max(initial=0)), 0), self.coded_ws, handle)
 
     def code_all(self, stream=None):
         """Codes every complete group of every history (once per history)."""
