@@ -353,6 +353,85 @@ def test_weights_of_many_shared_histories(whole):
     assert torch.equal(t["weights"], again)
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("vis,q_heads,kv", [([3, 2, 1, 3, 0], 2, 1), ([1029, 1027, 1025], 80, 8), ([67, 0, 3], 130, 65)])
+def test_weights_of_raw_tails_alone_and_of_many_heads(vis, q_heads, kv, whole, shared):
+    """Histories without a complete group, and more heads than a block of threads has statistics for."""
+    need_gpu()
+    h = ch.History(vis, q_heads=q_heads, kv_heads=kv, head_dim=64, fmt=ch.E4M3, seed=33, shared=shared)
+    t = ch.device(h, budget=7, whole=whole, weights=True)
+    ch.fill_cache(h, t)
+    rows = None if whole else ch.some_rows(h, 7, 34)
+    ids, n = (None, None) if whole else ch.rows_to_device(rows, 7)
+    ref, share, tol, rel = ch.attention(h, rows)
+    _close(h, _attend(t, ids, n, weights=True), ref, tol)
+    _ok(t)
+    # (a share sums up to 130 heads, not the 16 that the helper counts)
+    w, wt = ch.add_weights(h, share, [x + q_heads * 2.0 ** -24 for x in rel])
+    assert (np.abs(t["weights"].cpu().numpy() - w) <= wt).all()
+
+
+def test_the_longest_history():
+    """QSA_MAX_VISIBLE tokens less one beside a short history: 2^24 groups that name 61
+    blocks in turn, so that the result is a sum over 61 blocks with their counts.
+    The tokens of a run of 32,768 groups enter a warp's sums in 2,048 additions and
+    512 runs are merged by 64: each leaves half a step."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    nb, T = 61, 2 ** 26 - 1
+    G = T // 4
+    h = ch.History([4 * nb + 3, 4 * nb + 3], q_heads=2, kv_heads=1, head_dim=64, fmt=ch.E4M3, seed=35, shared=True)
+    t = ch.device(h, whole=True)
+    ch.fill_cache(h, t)
+    visible = torch.tensor([T, 4 * nb + 3], dtype=torch.int32, device="cuda")
+    block_map = torch.empty(G + nb, dtype=torch.int32, device="cuda")
+    block_map[:G] = t["block_map"][torch.arange(G, device="cuda") % nb]
+    block_map[G:] = t["block_map"]
+    block_offset = torch.tensor([0, G], dtype=torch.int64, device="cuda")
+    slot_map = torch.full((T + 4 * nb + 3,), -7, dtype=torch.int32, device="cuda")  # read for the raw tails alone
+    slot_map[T - 3:T] = t["slot_map"][4 * nb:]
+    slot_map[T + 4 * nb:] = t["slot_map"][4 * nb:]
+    slot_offset = torch.tensor([0, T], dtype=torch.int64, device="cuda")
+    weights = torch.zeros(G + 1 + nb + 1, device="cuda")
+    weight_offset = torch.tensor([0, G + 1], dtype=torch.int64, device="cuda")
+    dims = qsa.make_dims(2, 8, 64, 2, 1, 64, max_visible=2 ** 26, scale=h.scale)
+    ws = torch.zeros(qsa.qsa_coded_workspace_size(dims, True, True), dtype=torch.uint8, device="cuda")
+    inp = qsa.QsaInputs(visible=visible.data_ptr(), q=t["q"].data_ptr(), k_cache=t["k_cache"].data_ptr(),
+                        v_cache=t["v_cache"].data_ptr(), num_slots=h.num_slots, slot_map=slot_map.data_ptr(),
+                        slot_offset=slot_offset.data_ptr())
+    cache = qsa.QsaCodedCache.of(t["codes"], t["scales"], block_map, block_offset, h.fmt)
+    out = torch.full((2, 2, 64), float("nan"), device="cuda")
+    qsa.qsa_attend_coded(dims, inp, cache, None, None, out, ws, weights=weights, weight_offset=weight_offset)
+    assert qsa.qsa_check_errors(ws)[1] == 0
+    K, V = h.coded()
+    K = np.concatenate([K[:nb, 0].reshape(-1, 64), h.k[4 * nb:4 * nb + 3, 0]]).astype(np.float64)
+    V = np.concatenate([V[:nb, 0].reshape(-1, 64), h.v[4 * nb:4 * nb + 3, 0]]).astype(np.float64)
+    got, w = out.cpu().numpy(), weights.cpu().numpy().astype(np.float64)
+    rel = 2.0 ** -24 * (2 * (2048 + 64 + 16) + 4 * 30) + 2.0 ** -22 * 14 * 16
+    for b, groups in ((0, G), (1, nb)):
+        count = np.bincount(np.arange(groups) % nb, minlength=nb).astype(np.float64)
+        share = np.zeros(nb + 1)
+        for hd in range(2):
+            p = np.exp((h.q[b, hd].astype(np.float64) @ K.T) * h.scale)
+            n = np.concatenate([np.repeat(count, 4), np.ones(3)])
+            Z = (p * n).sum()
+            assert np.abs((np.abs(h.q[b, hd]) @ np.abs(K).T) * h.scale).max() < 16
+            assert np.abs(got[b, hd] - (p * n) @ V / Z).max() <= rel * np.abs(V).max()
+            share += np.concatenate([p[:4 * nb].reshape(nb, 4).sum(1), [p[4 * nb:].sum()]]) / Z
+        off = 0 if b == 0 else G + 1
+        want = np.concatenate([share[np.arange(groups) % nb], share[nb:]])
+        assert (np.abs(w[off:off + groups + 1] - want) <= rel * want).all()
+    # and its eviction, down to half
+    keep = G // 2
+    kept = torch.full((2, keep), -1, dtype=torch.int32, device="cuda")
+    n_kept = torch.zeros(2, dtype=torch.int32, device="cuda")
+    qsa.qsa_evict_select(dims, visible, weights, weight_offset, keep, 4, 1000, kept, n_kept, ws)
+    assert n_kept.tolist() == [keep, nb] and torch.equal(kept[1, :nb].cpu(), torch.arange(nb, dtype=torch.int32))
+    ref = ch.evict([T], w, [0], keep, 4, 1000)[0]
+    assert np.array_equal(kept[0].cpu().numpy(), ref)
+
+
 def test_an_output_does_not_depend_on_the_batch_or_the_workspace():
     """Each query alone, in a workspace made for its own length, gives the bits it
     gives in the batch, call after call."""
