@@ -455,6 +455,34 @@ def test_an_output_does_not_depend_on_the_batch_or_the_workspace():
 
 
 @pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("q_heads,kv,d", HEADS)
+def test_rows_of_one_run_give_the_same_bits_as_among_longer_ones(q_heads, kv, d, fmt):
+    """Calls whose rows are all short enough for one run: against 64 bits, and bit for
+    bit against the same rows in a call that allows longer ones."""
+    torch = need_gpu()
+    from top_group_sparse_gb300 import qsa
+    vis = [0, 1, 2, 3, 4, 5, 15, 16, 17, 63, 64, 66, 131, 252, 255, 256]
+    h = ch.History(vis, q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=36)
+    for rows in (None, ch.some_rows(h, 13, 37)):
+        budget = 13 if rows else 512
+        t = ch.device(h, budget=budget, whole=rows is None, max_visible=259)
+        ch.fill_cache(h, t)
+        ids, n = ch.rows_to_device(rows, budget) if rows else (None, None)
+        ref, _, tol, _ = ch.attention(h, rows)
+        _close(h, _attend(t, ids, n), ref, tol)
+        _ok(t)
+        short = t["out"].clone()
+        if rows:  # budgets of more than one run
+            budget = 80
+            ids, n = ch.rows_to_device(rows, budget)
+        dims = qsa.make_dims(h.B, 8, 64, q_heads, kv, d, budget_groups=budget, max_visible=9001, scale=h.scale)
+        ws = torch.zeros(qsa.qsa_coded_workspace_size(dims, rows is None), dtype=torch.uint8, device="cuda")
+        out = torch.full_like(short, float("nan"))
+        qsa.qsa_attend_coded(dims, t["inputs"], t["cache"], ids, n, out, ws)
+        assert torch.equal(out, short)
+
+
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
 def test_wide_ranges_of_scales_and_scores(fmt):
     """Scores spread over hundreds (one token takes all the weight), queries and
     groups whose sizes differ by 2^40, zero queries."""

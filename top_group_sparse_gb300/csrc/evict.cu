@@ -23,8 +23,8 @@ namespace cg = cooperative_groups;
 // shared memory -- those also say how many keys above and equal to K the slices
 // before it hold, where a CTA's output begins -- so the whole choice is one launch
 // with one cluster barrier per pass and no workspace.  Latency bound: 65,536
-// groups 26 us, of which a cluster that has next to nothing to do takes 13; so
-// histories of up to kOneCta groups take one CTA and no cluster (6.4 us).
+// groups 25.6 us, of which a cluster that has next to nothing to do takes 13; so
+// histories of up to kOneCta groups take one CTA and no cluster (6.0 us).
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
