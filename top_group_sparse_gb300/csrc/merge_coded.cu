@@ -47,8 +47,8 @@ __device__ __forceinline__ float inverse(float L)  // of a denominator; 0: no to
 template <int D>
 __device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, int u, const Row &row)
 {
-    constexpr int kPer = 2;
     constexpr int kHalves = D / 64;
+    constexpr int kNext = 4;
     const int h = u / kHalves, col = (u % kHalves) * 32 + (threadIdx.x & 31);
     const int lane = threadIdx.x & 31;
     const int used = used_runs(a, row);
@@ -56,10 +56,13 @@ __device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, i
     const float2 *src = reinterpret_cast<const float2 *>(a.part_acc + hb * a.nparts * D) + col;
     const float pm = lane < used ? __ldcg(a.part_m + hb * a.nparts + lane) : -INFINITY;
     const float pl = lane < used ? __ldcg(a.part_l + hb * a.nparts + lane) : 0.0f;
-    float2 x[kSlices];
+    // (the first twelve runs' dims are on their way before the first is used)
+    float2 sum[kSlices], next[kNext];
 #pragma unroll
-    for (int s = 0; s < kSlices; ++s)
-        if (s < used) x[s] = __ldcg(src + int64_t(s) * (D / 2));
+    for (int s = 0; s < kSlices; ++s) sum[s] = s < used ? __ldcg(src + int64_t(s) * (D / 2)) : make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < kNext; ++k)
+        if (kSlices + k < used) next[k] = __ldcg(src + int64_t(kSlices + k) * (D / 2));
     float m = pm;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -68,32 +71,27 @@ __device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, i
     float L = lane < used ? fmaf(pl, w, 0.0f) : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    float sum[kSlices][kPer];
 #pragma unroll
-    for (int s = 0; s < kSlices; ++s)
+    for (int s = 0; s < kSlices; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        sum[s] = make_float2(fmaf(sum[s].x, ws, 0.0f), fmaf(sum[s].y, ws, 0.0f));
+    }
+    for (int c0 = kSlices; c0 < used; c0 += kSlices) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) sum[s][j] = 0.0f;
-    for (int c0 = 0; c0 < used; c0 += kSlices) {
+        for (int s0 = 0; s0 < kSlices; s0 += kNext) {
 #pragma unroll
-        for (int s = 0; s < kSlices; ++s) {
-            const float ws = __shfl_sync(0xffffffffu, w, (c0 + s) & 31);
-            if (c0 + s < used) {
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) sum[s][j] = fmaf(at(x[s], j), ws, sum[s][j]);
+            for (int k = 0; k < kNext; ++k) {
+                const int c = c0 + s0 + k;
+                const float ws = __shfl_sync(0xffffffffu, w, c & 31);
+                if (c < used) sum[s0 + k] = make_float2(fmaf(next[k].x, ws, sum[s0 + k].x), fmaf(next[k].y, ws, sum[s0 + k].y));
+                if (c + kNext < used) next[k] = __ldcg(src + int64_t(c + kNext) * (D / 2));
             }
         }
-#pragma unroll
-        for (int s = 0; s < kSlices; ++s)
-            if (c0 + kSlices + s < used) x[s] = __ldcg(src + int64_t(c0 + kSlices + s) * (D / 2));
     }
-    float2 out;
+    float2 out = sum[0];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        float o = sum[0][j];
-#pragma unroll
-        for (int s = 1; s < kSlices; ++s) o += sum[s][j];
-        at(out, j) = L > 0.0f || L != L ? o / L : 0.0f;
-    }
+    for (int s = 1; s < kSlices; ++s) out = make_float2(out.x + sum[s].x, out.y + sum[s].y);
+    out = L > 0.0f || L != L ? make_float2(out.x / L, out.y / L) : make_float2(0.0f, 0.0f);
     reinterpret_cast<float2 *>(a.out + hb * D)[col] = out;
     if (a.stat != nullptr && col == 0) reinterpret_cast<float2 *>(a.stat)[hb] = make_float2(M, inverse(L));
 }
@@ -198,7 +196,7 @@ constexpr int kStatHeads = 64;                         // heads whose M and 1/L 
 constexpr int kSharedSlices = 8;                       // threads per group, an eighth of the queries each
 constexpr int kSharedGroups = kAccThreads / kSharedSlices;
 constexpr int kList = 512;                             // queries of a history in hand at a time
-constexpr int kSharedCtas = 912;                       // 6 per SM; the sums do not depend on it
+constexpr int kSharedCtas = 608;                       // 4 per SM; the sums do not depend on it
 
 // M and 1/L of a head from its runs' states, by a warp.
 __device__ __forceinline__ float2 stat_of_runs(const AttendCodedArgs &a, int64_t hb, int used)
@@ -272,14 +270,17 @@ __device__ __forceinline__ void own_weights(const AttendCodedArgs &a, int b, int
     }
 }
 
-template <int D, bool kByWarp>
-__global__ void __launch_bounds__(kMergeThreads, 4) merge_coded_kernel(const AttendCodedArgs a, int merge_ctas)
+// CTAs per SM: without the weights' code there are registers for five (1,024 queries of
+// two runs, 16 heads x 128: 13.5 -> 12.1 us; six take 11.7, but 12 queries of 18 runs
+// 4.7 instead of 3.4, too few of their loads being under way at a time).
+template <int D, bool kByWarp, bool kOwn>
+__global__ void __launch_bounds__(kMergeThreads, kByWarp && !kOwn ? 5 : 4) merge_coded_kernel(const AttendCodedArgs a, int merge_ctas)
 {
     const int x = blockIdx.x, b = blockIdx.y;
     wait_for_predecessor();
     const Row row = row_of(a, b);
-    if (x >= merge_ctas) {
-        own_weights(a, b, x - merge_ctas, int(gridDim.x) - merge_ctas, row);
+    if (kOwn && x >= merge_ctas) {
+        if constexpr (kOwn) own_weights(a, b, x - merge_ctas, int(gridDim.x) - merge_ctas, row);
     } else if constexpr (kByWarp) {
         const int u = x * kMergeWarps + (threadIdx.x >> 5);
         if (u < a.q_heads * (D / 64)) merge_by_warp<D>(a, b, u, row);
@@ -311,10 +312,11 @@ __device__ __forceinline__ float share_of(const AttendCodedArgs &a, int b, int p
 // all the groups that it takes of it.  The list leaves out the batch's other queries:
 // a sum depends on the queries of its history alone.  It holds kList queries; those
 // of a larger history are added a list at a time.  64 histories of 2,048
-// groups and 4 queries each: 9.7 us for selected rows, 72 us for whole ones; with a
+// groups and 4 queries each: 7.7 us for selected rows, 26 us for whole ones (four CTAs
+// per SM; with six 9.7 and 72: too few registers for the loads in flight); with a
 // block of groups per CTA and a pass over the whole batch for each history 222 and 482.
 template <bool kWhole>
-__global__ void __launch_bounds__(kAccThreads, 6) shared_weights_kernel(const AttendCodedArgs a)
+__global__ void __launch_bounds__(kAccThreads, 4) shared_weights_kernel(const AttendCodedArgs a)
 {
     __shared__ int2 list[kList + kAccThreads];  // a query, and 2 * its history's groups + (it has a raw tail)
     __shared__ float sum[kSharedSlices][kSharedGroups];
@@ -443,30 +445,29 @@ __global__ void __launch_bounds__(kAccThreads, 6) shared_weights_kernel(const At
     }
 }
 
-template <int D>
+template <int D, bool kOwn>
 cudaError_t launch_merge_t(const AttendCodedArgs &a, cudaStream_t s)
 {
     int own = 0;
-    if (a.weights != nullptr) {
+    if (kOwn) {
         const int positions = (a.ids == nullptr ? a.max_visible : a.row_cap) / kGroup + 1;
         own = (positions + kOwnPos - 1) / kOwnPos;
         if (own > 1024) own = 1024;
     }
-    if (a.nparts <= kWarpRuns) {
-        const int ctas = (a.q_heads * (D / 64) + kMergeWarps - 1) / kMergeWarps;
-        return launch_kernel(merge_coded_kernel<D, true>, dim3(unsigned(ctas + own), unsigned(a.batch)), dim3(kMergeThreads), 0, s,
-                             true, a, ctas);
-    }
-    return launch_kernel(merge_coded_kernel<D, false>, dim3(unsigned(a.q_heads + own), unsigned(a.batch)), dim3(kMergeThreads), 0,
-                         s, true, a, a.q_heads);
+    const bool by_warp = a.nparts <= kWarpRuns;
+    const int ctas = by_warp ? (a.q_heads * (D / 64) + kMergeWarps - 1) / kMergeWarps : a.q_heads;
+    return launch_kernel(by_warp ? merge_coded_kernel<D, true, kOwn> : merge_coded_kernel<D, false, kOwn>,
+                         dim3(unsigned(ctas + own), unsigned(a.batch)), dim3(kMergeThreads), 0, s, true, a, ctas);
 }
 
 }  // namespace
 
 cudaError_t launch_merge_coded(const AttendCodedArgs &a, cudaStream_t s)
 {
-    cudaError_t e = a.head_dim == 128 ? launch_merge_t<128>(a, s) : launch_merge_t<64>(a, s);
-    if (e != cudaSuccess || a.weights == nullptr || a.batch == 1) return e;
+    const bool own = a.weights != nullptr;
+    const cudaError_t e = a.head_dim == 128 ? (own ? launch_merge_t<128, true>(a, s) : launch_merge_t<128, false>(a, s))
+                                            : (own ? launch_merge_t<64, true>(a, s) : launch_merge_t<64, false>(a, s));
+    if (e != cudaSuccess || !own || a.batch == 1) return e;
     const int64_t most = int64_t(a.max_visible / kGroup + kSharedGroups) / kSharedGroups * (a.batch / 2);  // units
     return launch_kernel(a.ids == nullptr ? shared_weights_kernel<true> : shared_weights_kernel<false>,
                          dim3(unsigned(most < kSharedCtas ? most : kSharedCtas)), dim3(kAccThreads), 0, s, true, a);
