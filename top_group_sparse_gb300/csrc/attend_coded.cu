@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
     const int part = int(blockIdx.x) - extra, kvh = blockIdx.y, b = blockIdx.z;
     const int h0 = kvh * gq;
     if (part == -2 && kvh != 0) return;
+    const int64_t block_offset = __ldg(a.block_offset + b);  // (under way while the row is looked up)
     const Row row = row_of(a, b);
     if (part < 0) {
         if (part == -2) {
@@ -327,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
         float4 *map = reinterpret_cast<float4 *>(a.share_map + int64_t(b) * a.map_stride);
         for (int g = g0 + tid; g < min(g0 + n, a.map_stride / 4); g += kThreads) map[g] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int64_t block_offset = __ldg(a.block_offset + b);
     const int per_run = coded_run_groups(row.groups, whole, gq);
     const int run_begin = part * per_run, run_end = min(row.groups, run_begin + per_run);
     if (run_begin >= run_end) return;
