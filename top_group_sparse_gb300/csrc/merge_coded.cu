@@ -43,26 +43,32 @@ __device__ __forceinline__ float inverse(float L)  // of a denominator; 0: no to
     return L > 0.0f || L != L ? 1.0f / L : 0.0f;
 }
 
-// Unit u: 64 dims of head u / (D/64), two a lane.
+// Unit u: 64 dims of head u / (D/64), two a lane.  The states are loaded before the row's
+// length is known: `most` bounds the runs of the call's rows, and what is behind this
+// row's runs is not used.
 template <int D>
-__device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, int u, const Row &row)
+__device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, int u, int most)
 {
     constexpr int kHalves = D / 64;
     constexpr int kNext = 4;
     const int h = u / kHalves, col = (u % kHalves) * 32 + (threadIdx.x & 31);
     const int lane = threadIdx.x & 31;
-    const int used = used_runs(a, row);
     const int64_t hb = int64_t(b) * a.q_heads + h;
     const float2 *src = reinterpret_cast<const float2 *>(a.part_acc + hb * a.nparts * D) + col;
-    const float pm = lane < used ? __ldcg(a.part_m + hb * a.nparts + lane) : -INFINITY;
-    const float pl = lane < used ? __ldcg(a.part_l + hb * a.nparts + lane) : 0.0f;
-    // (the first twelve runs' dims are on their way before the first is used)
+    float pm = -INFINITY, pl = 0.0f;
+    if (lane < most) {
+        pm = __ldcg(a.part_m + hb * a.nparts + lane);
+        pl = __ldcg(a.part_l + hb * a.nparts + lane);
+    }
     float2 sum[kSlices], next[kNext];
 #pragma unroll
-    for (int s = 0; s < kSlices; ++s) sum[s] = s < used ? __ldcg(src + int64_t(s) * (D / 2)) : make_float2(0.0f, 0.0f);
+    for (int s = 0; s < kSlices; ++s)
+        if (s < most) sum[s] = __ldcg(src + int64_t(s) * (D / 2));
 #pragma unroll
     for (int k = 0; k < kNext; ++k)
-        if (kSlices + k < used) next[k] = __ldcg(src + int64_t(kSlices + k) * (D / 2));
+        if (kSlices + k < most) next[k] = __ldcg(src + int64_t(kSlices + k) * (D / 2));
+    const int used = used_runs(a, row_of(a, b));
+    if (lane >= used) pm = -INFINITY;
     float m = pm;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -74,7 +80,7 @@ __device__ __forceinline__ void merge_by_warp(const AttendCodedArgs &a, int b, i
 #pragma unroll
     for (int s = 0; s < kSlices; ++s) {
         const float ws = __shfl_sync(0xffffffffu, w, s);
-        sum[s] = make_float2(fmaf(sum[s].x, ws, 0.0f), fmaf(sum[s].y, ws, 0.0f));
+        sum[s] = s < used ? make_float2(fmaf(sum[s].x, ws, 0.0f), fmaf(sum[s].y, ws, 0.0f)) : make_float2(0.0f, 0.0f);
     }
     for (int c0 = kSlices; c0 < used; c0 += kSlices) {
 #pragma unroll
@@ -274,18 +280,18 @@ __device__ __forceinline__ void own_weights(const AttendCodedArgs &a, int b, int
 // two runs, 16 heads x 128: 13.5 -> 12.1 us; six take 11.7, but 12 queries of 18 runs
 // 4.7 instead of 3.4, too few of their loads being under way at a time).
 template <int D, bool kByWarp, bool kOwn>
-__global__ void __launch_bounds__(kMergeThreads, kByWarp && !kOwn ? 5 : 4) merge_coded_kernel(const AttendCodedArgs a, int merge_ctas)
+__global__ void __launch_bounds__(kMergeThreads, kByWarp && !kOwn ? 5 : 4)
+merge_coded_kernel(const AttendCodedArgs a, int merge_ctas, int most)
 {
     const int x = blockIdx.x, b = blockIdx.y;
     wait_for_predecessor();
-    const Row row = row_of(a, b);
     if (kOwn && x >= merge_ctas) {
-        if constexpr (kOwn) own_weights(a, b, x - merge_ctas, int(gridDim.x) - merge_ctas, row);
+        if constexpr (kOwn) own_weights(a, b, x - merge_ctas, int(gridDim.x) - merge_ctas, row_of(a, b));
     } else if constexpr (kByWarp) {
         const int u = x * kMergeWarps + (threadIdx.x >> 5);
-        if (u < a.q_heads * (D / 64)) merge_by_warp<D>(a, b, u, row);
+        if (u < a.q_heads * (D / 64)) merge_by_warp<D>(a, b, u, most);
     } else {
-        merge_by_block<D>(a, b, x, row);
+        merge_by_block<D>(a, b, x, row_of(a, b));
     }
 }
 
@@ -454,10 +460,12 @@ cudaError_t launch_merge_t(const AttendCodedArgs &a, cudaStream_t s)
         own = (positions + kOwnPos - 1) / kOwnPos;
         if (own > 1024) own = 1024;
     }
-    const bool by_warp = a.nparts <= kWarpRuns;
+    const bool whole = a.ids == nullptr;
+    const int most = whole ? a.nparts : coded_runs((a.row_cap - (kGroup - 1)) / kGroup, false, a.q_heads / a.kv_heads) + 1;
+    const bool by_warp = most <= kWarpRuns;
     const int ctas = by_warp ? (a.q_heads * (D / 64) + kMergeWarps - 1) / kMergeWarps : a.q_heads;
     return launch_kernel(by_warp ? merge_coded_kernel<D, true, kOwn> : merge_coded_kernel<D, false, kOwn>,
-                         dim3(unsigned(ctas + own), unsigned(a.batch)), dim3(kMergeThreads), 0, s, true, a, ctas);
+                         dim3(unsigned(ctas + own), unsigned(a.batch)), dim3(kMergeThreads), 0, s, true, a, ctas, most);
 }
 
 }  // namespace
