@@ -15,7 +15,7 @@ namespace {
 // Rows of at most 32 runs: a warp per head and 64 dims, eight a CTA.  Longer ones: a
 // CTA per head.  Both add in the same order -- eight sums over the runs c = s,
 // s+8, .. (s < 8), added in order of s -- so that a row's bits do not depend on
-// which of the two its batch takes.  Latency bound (2.5 us for 8 rows of 8 runs,
+// which of the two its batch takes.  Latency bound (2.1 us for 8 rows of 8 runs,
 // 6.8 us for 8 rows of 256): every load that can be is made before the first is
 // used.  Launching it early, to wait resident beside the runs' CTAs, took 2-5 us
 // more than its launch saved.
