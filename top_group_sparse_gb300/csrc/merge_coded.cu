@@ -190,17 +190,17 @@ __device__ __forceinline__ void merge_by_block(const AttendCodedArgs &a, int b, 
 // No atomics: a query with accumulators of its own adds its shares as they come
 // (own_weights, CTAs beside the merge's, which find M and L themselves from the
 // runs' states rather than wait for the merge); queries that share accumulators
-// are added in a fixed order, eight threads per group (shared_weights_kernel), so
+// are added in a fixed order, up to 32 partial sums per group (shared_weights_kernel), so
 // that the sum has one value.  Selected rows of such queries are first spread out
 // to one share per group of the history (in the workspace's scores, which nobody
 // needs by then), so that the second kernel reads rows side by side: on 256
 // queries that share a history of 25,064 groups, searching each group in each
-// query's row instead took 1540 us, this 16 us.
+// query's row instead took 1540 us, this 14 us.
 constexpr int kAccThreads = kMergeThreads;
 constexpr int kOwnPos = kAccThreads;                   // positions of a CTA, one per thread
 constexpr int kStatHeads = 64;                         // heads whose M and 1/L are in hand at a time
-constexpr int kSharedSlices = 8;                       // threads per group, an eighth of the queries each
-constexpr int kSharedGroups = kAccThreads / kSharedSlices;
+constexpr int kSharedGroups = 32;                      // groups of a unit of work
+constexpr int kManySlices = 32, kFewSlices = 8;        // parts of a sum over queries: of more than eight, of up to eight
 constexpr int kList = 512;                             // queries of a history in hand at a time
 constexpr int kSharedCtas = 608;                       // 4 per SM; the sums do not depend on it
 
@@ -295,20 +295,23 @@ merge_coded_kernel(const AttendCodedArgs a, int merge_ctas, int most)
     }
 }
 
-// Heads h0, h0 + step, .. of position pos.
-__device__ __forceinline__ float share_of(const AttendCodedArgs &a, int b, int pos, int h0, int step)
+// Groups g .. g+3 of a whole history, whose masses have one reference.
+__device__ __forceinline__ float4 shares_of(const AttendCodedArgs &a, int b, int g)
 {
-    float s = 0.0f;
-    const int64_t hb = int64_t(b) * a.q_heads;
-    const float *mass = a.mass + hb * a.mass_stride + pos;
-    const float *mref = a.mref + hb * (a.mass_stride / 4) + pos / 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int64_t hb = int64_t(b) * a.q_heads, step = a.mass_stride / 4;
+    const float4 *mass = reinterpret_cast<const float4 *>(a.mass + hb * a.mass_stride + g);
+    const float *mref = a.mref + hb * step + g / 4;
     const float2 *stat = reinterpret_cast<const float2 *>(a.stat) + hb;
 #pragma unroll 4
-    for (int h = h0; h < a.q_heads; h += step) {
+    for (int h = 0; h < a.q_heads; ++h) {
+        const float4 m = __ldcg(mass + h * step);
         const float2 st = __ldcg(stat + h);
-        const float g = __ldcg(mass + int64_t(h) * a.mass_stride);
-        const float r = __ldcg(mref + int64_t(h) * (a.mass_stride / 4));
-        s = fmaf(g * ex2(r - st.x), st.y, s);
+        const float e = ex2(__ldcg(mref + h * step) - st.x);
+        s.x = fmaf(m.x * e, st.y, s.x);
+        s.y = fmaf(m.y * e, st.y, s.y);
+        s.z = fmaf(m.z * e, st.y, s.z);
+        s.w = fmaf(m.w * e, st.y, s.w);
     }
     return s;
 }
@@ -318,19 +321,20 @@ __device__ __forceinline__ float share_of(const AttendCodedArgs &a, int b, int p
 // all the groups that it takes of it.  The list leaves out the batch's other queries:
 // a sum depends on the queries of its history alone.  It holds kList queries; those
 // of a larger history are added a list at a time.  64 histories of 2,048
-// groups and 4 queries each: 7.7 us for selected rows, 26 us for whole ones (four CTAs
-// per SM; with six 9.7 and 72: too few registers for the loads in flight); with a
-// block of groups per CTA and a pass over the whole batch for each history 222 and 482.
+// groups and 4 queries each: 8.2 us for selected rows, 19 us for whole ones (four CTAs
+// per SM, four groups a thread; one group a thread 7.7 and 26, and 16 instead of 14 on
+// 256 queries of one history; with six CTAs 9.7 and 72: too few registers for the loads
+// in flight); with a block of groups per CTA and a pass over the whole batch for each
+// history 222 and 482.
 template <bool kWhole>
 __global__ void __launch_bounds__(kAccThreads, 4) shared_weights_kernel(const AttendCodedArgs a)
 {
     __shared__ int2 list[kList + kAccThreads];  // a query, and 2 * its history's groups + (it has a raw tail)
-    __shared__ float sum[kSharedSlices][kSharedGroups];
+    __shared__ float4 sum[kAccThreads];
     __shared__ uint32_t marked[kAccThreads / 32];
     __shared__ int found;
-    constexpr int kAhead = 16;                  // shares loaded before they are added
+    constexpr int kAhead = 4;                   // loads made before the first is added
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int lg = tid % kSharedGroups, slice = tid / kSharedGroups;
     const int groups = a.max_visible / kGroup + 1;
     const int per_history = (groups + kSharedGroups - 1) / kSharedGroups;
     wait_for_predecessor();
@@ -350,55 +354,57 @@ __global__ void __launch_bounds__(kAccThreads, 4) shared_weights_kernel(const At
         }
         return before;
     };
-    // what query list[j] adds to group g
-    auto tail_of = [&](int2 m, int g) { return m.y == 2 * g + 1 ? __ldcg(a.tail_share + m.x) : 0.0f; };
-    auto mapped = [&](int2 m, int g) { return __ldcg(a.share_map + int64_t(m.x) * a.map_stride + min(g, a.map_stride - 1)); };
-
-    // blocks blk0 .. blk1 of the history of `off`: the first n queries of the list added
+    // blocks blk0 .. blk1 of the history of `off`: the first n queries of the list added, in
+    // `slices` sums over the queries k, k + slices, .. that are added in order of k.  (Up
+    // to eight queries are one to a sum either way.)
     auto add_list = [&](int64_t off, int blk0, int blk1, int n) {
-        if (n <= kSharedSlices && blk1 - blk0 > 1) {  // few queries, many groups: a thread per group
-            const int end = min(blk1 * kSharedGroups, groups);
-            for (int g = blk0 * kSharedGroups + tid; g < end; g += kAccThreads) {
-                float t[kSharedSlices], s = 0.0f;
+        const int slices = n <= kFewSlices ? kFewSlices : kManySlices, quads = kAccThreads / slices;
+        const int slice = tid / quads, quad = tid % quads;
+        const int end = min(blk1 * kSharedGroups, groups);
+        for (int g0 = blk0 * kSharedGroups; g0 < end; g0 += 4 * quads) {
+            const int g = g0 + 4 * quad;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            auto add = [&](const float4 &t, int history) {
+                s.x += g < history ? t.x : 0.0f;
+                s.y += g + 1 < history ? t.y : 0.0f;
+                s.z += g + 2 < history ? t.z : 0.0f;
+                s.w += g + 3 < history ? t.w : 0.0f;
+            };
+            if (g < end) {
+                if constexpr (kWhole) {
+                    for (int j = slice; j < n; j += slices)
+                        if (g < list[j].y / 2) add(shares_of(a, list[j].x, g), list[j].y / 2);
+                } else {
+                    const float *map = a.share_map + min(g, a.map_stride - 4);
+                    for (int j = slice; j < n; j += slices * kAhead) {
+                        float4 t[kAhead];
 #pragma unroll
-                for (int j = 0; j < kSharedSlices; ++j) {  // (the order of the sums below)
-                    if (j >= n) continue;
-                    const int2 m = list[j];
-                    t[j] = g < m.y / 2 ? (kWhole ? share_of(a, m.x, g, 0, 1) : mapped(m, g)) : tail_of(m, g);
+                        for (int u = 0; u < kAhead; ++u)  // (every load is made, no branch between them)
+                            t[u] = __ldcg(reinterpret_cast<const float4 *>(map + int64_t(list[min(j + u * slices, n - 1)].x) * a.map_stride));
+#pragma unroll
+                        for (int u = 0; u < kAhead; ++u)
+                            if (j + u * slices < n) add(t[u], list[j + u * slices].y / 2);
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < kSharedSlices; ++j)
-                    if (j < n) s += t[j];
-                if (s != 0.0f) a.weights[off + g] += s;
-            }
-            return;
-        }
-        for (int blk = blk0; blk < blk1; ++blk) {
-            const int g = blk * kSharedGroups + lg;
-            float s = 0.0f;
-            if constexpr (kWhole) {
-                for (int j = slice; j < n; j += kSharedSlices)
-                    if (g < list[j].y / 2) s += share_of(a, list[j].x, g, 0, 1);
-            } else {
-                for (int j = slice; j < n; j += kSharedSlices * kAhead) {
-                    float t[kAhead];
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u)  // (every load is made, no branch between them)
-                        t[u] = mapped(list[min(j + u * kSharedSlices, n - 1)], g);
-#pragma unroll
-                    for (int u = 0; u < kAhead; ++u) {
-                        const int o = j + u * kSharedSlices;
-                        if (o < n && g < list[o].y / 2) s += t[u];
+                for (int j = slice; j < n; j += slices) {  // the raw tails
+                    const int2 m = list[j];
+                    if ((m.y & 1) && (m.y / 2 & ~3) == g) {
+                        const float t = __ldcg(a.tail_share + m.x);
+                        const int at = m.y / 2 - g;
+                        s.x += at == 0 ? t : 0.0f;
+                        s.y += at == 1 ? t : 0.0f;
+                        s.z += at == 2 ? t : 0.0f;
+                        s.w += at == 3 ? t : 0.0f;
                     }
                 }
             }
-            for (int j = slice; j < n; j += kSharedSlices) s += tail_of(list[j], g);
-            sum[slice][lg] = s;
+            sum[tid] = s;  // [slices][quads]
             __syncthreads();
-            if (slice == 0) {
-#pragma unroll
-                for (int k = 1; k < kSharedSlices; ++k) s += sum[k][lg];
-                if (s != 0.0f) a.weights[off + g] += s;
+            if (tid < 4 * quads && g0 + tid < end) {
+                const float *part = reinterpret_cast<const float *>(sum) + tid;
+                float w = part[0];
+                for (int k = 1; k < min(n, slices); ++k) w += part[k * 4 * quads];
+                if (w != 0.0f) a.weights[off + g0 + tid] += w;
             }
             __syncthreads();
         }
