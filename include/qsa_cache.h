@@ -93,8 +93,9 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  *     QSA_MAX_VISIBLE).
  * Groups are read from the coded cache, the last (row length mod 4) tokens
  * from the f32 k_cache / v_cache through the slot map.  An empty row gives a
- * zero output.  Reads in->q, visible, slot_map, slot_offset, k_cache, v_cache.
- * out: [B, n_q, d].
+ * zero output, and so does a head whose scores are all -inf (below binary32's
+ * range), which adds no weight either.  Reads in->q, visible, slot_map,
+ * slot_offset, k_cache, v_cache.  out: [B, n_q, d].
  *
  * weights (NULL: none): accumulated attention.  weights[weight_offset[b] + g]
  * += sum over heads h and over the row's tokens t of group g = t/4 of

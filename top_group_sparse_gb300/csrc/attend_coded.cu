@@ -616,7 +616,9 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                 if (a.mass != nullptr && h < gq) {
                     const int64_t hb = int64_t(b) * a.q_heads + h0 + h;
                     if (meta.w == 0.0f) a.mass[hb * a.mass_stride + seg + g0 + i4] = gs;
-                    if (i4 == 0) a.mref[hb * (a.mass_stride / 4) + (seg + g0) / 4] = ms;
+                    // (m_run itself: while it is -inf the masses are 0, and 2^(-inf - M) is 0 for every
+                    // M, where 2^(0 - M) is infinite for M below -128 and would make the share NaN)
+                    if (i4 == 0) a.mref[hb * (a.mass_stride / 4) + (seg + g0) / 4] = m_run[s];
                 }
             }
 
