@@ -1,5 +1,6 @@
 """Where the numbers of the coded cache are hardest to keep, against the plain forms
-in 64 bits (tests/cache_helpers.py): scores that leave binary32."""
+in 64 bits (tests/cache_helpers.py): scores that leave binary32 or come near, values of
+neighbouring groups whose sizes differ."""
 import numpy as np
 import pytest
 
@@ -75,3 +76,117 @@ def test_scores_of_minus_infinity_get_no_weight(q_heads, kv, d, fmt, whole, shar
     assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()
     untouched = w == h.weights0
     assert untouched.any() and (got[untouched] == h.weights0[untouched]).all()
+
+
+# ---- values of neighbouring groups that differ in size -----------------------------------
+
+def _bound(h, b, hd, row, K, V, same_scores=False):
+    """(output of head hd over a row of whole groups, its tolerance per dim) in 64 bits.
+
+    A weight p * sV enters as two 16-bit floats under a power of two that brings the
+    largest of its head's in the step (four consecutive groups of the row) to 2^12 or
+    more: it keeps 22 bits, or 2^-25 of that scale, i.e. 2^-37 of the largest.  All other
+    errors are relative to the sum of |p v| in the dim itself: 2^-22 * (14 S + 30) as
+    derived in cache_helpers.attention, without S where the scores' errors cancel."""
+    kv = hd // (h.q_heads // h.kv_heads)
+    g = h.group_offset[b] + row[::4] // 4
+    k, v = K[g, kv].reshape(-1, h.d), V[g, kv].reshape(-1, h.d)
+    q = h.q[b, hd].astype(np.float64)
+    x = (k @ q) * h.scale
+    S = 0.0 if same_scores else float((np.abs(k) @ np.abs(q)).max()) * h.scale
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    sv = ch.encode(h.v[h.token_offset[b] + 4 * (row[::4] // 4)[:, None] + np.arange(4)][:, :, kv], h.fmt)[1].astype(np.float64)
+    w = p * np.repeat(sv, 4)
+    pad = -len(w) % 16
+    step = np.concatenate([w, np.zeros(pad)]).reshape(-1, 16).max(axis=1)
+    codes = np.abs(v) / np.repeat(np.where(sv > 0, sv, 1), 4)[:, None]
+    tol = 2.0 ** -22 * (14 * S + 30) * (p @ np.abs(v)) + 2.0 ** -37 * (np.repeat(step, 16)[:len(w)] @ codes)
+    return p @ v, tol
+
+
+def _check_per_dim(h, rows, whole, same_scores):
+    K, V = h.coded()
+    out, _, flags = _attend(h, None if whole else rows)
+    assert flags == 0 and np.isfinite(out).all()
+    for b in range(h.B):
+        for hd in range(h.q_heads):
+            want, tol = _bound(h, b, hd, rows[b], K, V, same_scores)
+            err = np.abs(out[b, hd] - want)
+            assert (err <= tol).all(), (b, hd, (err / tol).max(), (err / np.abs(want).max()).max())
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("q_heads,kv,d", HEADS)
+@pytest.mark.parametrize("exponent", [0, 80, -80])
+def test_a_small_group_that_takes_the_weight_beside_large_ones(exponent, q_heads, kv, d, fmt, whole):
+    """One group takes the weight, its values 2^-4 .. 2^-32 of its step neighbours', whose
+    weights are below 2^-60 of its own.  Its four tokens have one value, so the output is
+    that value whatever the scores' errors do to their weights."""
+    need_gpu()
+    r = np.random.RandomState(3)
+    ratios = [4, 12, 16, 20, 24, 32]
+    groups = [40, 77, 100, 64, 300, 13]
+    h = ch.History([4 * g for g in groups], q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=4)
+    u = r.choice([-1.0, 1.0], (kv, d)).astype(np.float32)
+    h.q[:] = np.repeat(u, q_heads // kv, axis=0)[None]
+    h.k[:] = -3 * u
+    for b, (n, ratio) in enumerate(zip(groups, ratios)):
+        t = h.token_offset[b] + 4 * r.randint(n)
+        h.k[t:t + 4] = 3 * u
+        h.v[t:t + 4] = h.v[t] * np.float32(2.0 ** -ratio)
+    h.v *= np.float32(2.0 ** exponent)
+    _set_cache(h)
+    _check_per_dim(h, [np.arange(4 * g) for g in groups], whole, True)
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("q_heads,kv,d", HEADS)
+def test_groups_that_weigh_the_more_the_smaller_they_are(q_heads, kv, d, fmt, whole):
+    """Values of 2^-r and weights near 2^r, r from 0 to 24 from group to group (and some
+    groups of zeros): all contribute alike."""
+    need_gpu()
+    r = np.random.RandomState(5)
+    groups = [130, 512, 7, 64]
+    h = ch.History([4 * g for g in groups], q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=6)
+    u = r.choice([-1.0, 1.0], (kv, d)).astype(np.float32)
+    h.q[:] = np.repeat(u, q_heads // kv, axis=0)[None] * (0.75 + 0.5 * r.rand(1, q_heads, 1)).astype(np.float32)
+    e = np.repeat(r.randint(0, 25, sum(groups)), 4)
+    h.k[:] = u * (e * np.log(2) / (h.scale * d))[:, None, None].astype(np.float32)
+    h.v *= (2.0 ** -e)[:, None, None].astype(np.float32)
+    h.v[np.repeat(r.rand(sum(groups)) < 0.1, 4)] = 0
+    _set_cache(h)
+    _check_per_dim(h, [np.arange(4 * g) for g in groups], whole, False)
+
+
+# ---- scores whose neighbours are 16 apart -------------------------------------------------
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("q_heads,kv,d", [(8, 1, 64), (16, 1, 64), (16, 2, 128), (16, 1, 128)])
+def test_scores_near_two_to_the_27(q_heads, kv, d, fmt, whole):
+    """Scores (base 2) between 2^27 and 2^28, where binary32's numbers are 16 apart and a
+    running maximum plus 8 may round to the next of them, so that a weight of 2^16
+    follows without a new maximum.  K scales that differ in the last bit give scores one
+    number apart.  What such scores' weights are is up to their rounding; the outputs
+    are averages of values all the same: each lies between the least and the largest of
+    its dim (30 * 2^-22: the sums' own rounding)."""
+    need_gpu()
+    r = np.random.RandomState(9)
+    G = 300
+    h = ch.History([4 * G], q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=10)
+    amp = 2.0 ** 27.3 / (d * h.scale * 1.4427) * (1 + np.arange(q_heads) / 32)
+    h.q[:] = amp[None, :, None].astype(np.float32)
+    up = np.where(np.arange(G) < 16, 0, r.randint(0, 2, G)).astype(np.uint32)
+    h.k[:] = np.repeat((np.float32(1).view(np.uint32) + up).view(np.float32), 4)[:, None, None]
+    _set_cache(h)
+    rows = None if whole else [np.arange(4 * G)]
+    out, _, flags = _attend(h, rows)
+    assert flags == 0 and np.isfinite(out).all()
+    V = h.coded()[1]
+    for hd in range(q_heads):
+        v = V[:, hd // (q_heads // kv)].reshape(-1, d)
+        slack = 30 * 2.0 ** -22 * np.abs(v).max()
+        assert (out[0, hd] <= v.max(axis=0) + slack).all() and (out[0, hd] >= v.min(axis=0) - slack).all()

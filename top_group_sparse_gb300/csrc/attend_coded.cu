@@ -8,9 +8,12 @@
 // over the runs of a row in a fixed order.
 //
 // An 8-bit code is exact in a 16-bit float, so both products run on the tensor
-// cores with operands that lose nothing: q and the weights w_t = p_t sV_g enter
-// as hi + lo, two 16-bit floats of 11 bits each, scaled by a power of two that
-// keeps both halves clear of the 16-bit subnormals where they matter.  The
+// cores with operands of 22 bits: q and the weights w_t = p_t sV_g enter as
+// hi + lo, two 16-bit floats of 11 bits each, under a power of two per head (q) or
+// per head and step (w) that brings the largest to 2^12 or more, so that what falls
+// among the 16-bit subnormals is below 2^-37 of it.  (A power of two per step alone,
+// from its largest sV, lost the groups that a head attends to beside larger ones:
+// 1 % of the output at sV 2^-24 of a neighbour's, all of it at 2^-32.)  The
 // matrix instruction m16n8k16 has 16 rows; with at most 8 query heads per KV
 // head, rows 0-7 hold the hi parts and rows 8-15 the lo parts of the same heads,
 // so one instruction does both and its two result rows h and h+8, which the same
@@ -67,7 +70,7 @@ struct Sm {
     static constexpr int kBlk = 8 * D + kBlkPad;
     static constexpr int kStage = kStepGroups * kBlk;
     alignas(128) unsigned char ring[kWarps][kRing][kStage];  // also the end-of-run reduction area
-    alignas(16) float4 meta[kSegGroups];                     // K scale, V scale * f, 1/f, 0 (-inf: no such group)
+    alignas(16) float4 meta[kSegGroups];                     // K scale, V scale and its exponent, 0 (-inf: no such group)
     alignas(16) uint4 qa[D / 16][HS][32];                    // each lane's operands of q (9-16 heads: hi, lo)
     float qs[8 * HS];                                        // 1/f of each head's q
     alignas(16) int blk[kSegGroups];                         // physical block; -1: none, -2: zero rows
@@ -159,18 +162,29 @@ __device__ __forceinline__ void split2(float2 v, uint32_t &hi, uint32_t &lo)
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// Powers of two that bring a largest magnitude (its bits) to [2^kTop / 2, 2^kTop),
-// and back.  The exponent is kept to -110..128, so that both are normal floats.
-constexpr int kQTop = 14;   // of q
-constexpr int kLag = 8;     // log2 of the largest softmax weight
-constexpr int kVTop = 6;    // of the V scales of a step: times a weight, below 2^14
-template <int kTop>
-__device__ __forceinline__ void scale_to(uint32_t top, float &f, float &inv)
+// The power of two that brings the largest magnitude of a head's q (its bits) to
+// [2^13, 2^14), and its inverse.  The exponent is kept to -110..128, so that both are
+// normal floats.
+__device__ __forceinline__ void scale_of_q(uint32_t top, float &f, float &inv)
 {
     const int e = max(int(top >> 23) - 127, -110);
-    f = __uint_as_float(uint32_t(kTop - 1 - e + 127) << 23);
-    inv = __uint_as_float(uint32_t(e - kTop + 1 + 127) << 23);
+    f = __uint_as_float(uint32_t(13 - e + 127) << 23);
+    inv = __uint_as_float(uint32_t(e - 13 + 127) << 23);
 }
+
+// The same for the weights of a head in a step, to [2^12, 2^15).  z: the largest sum of
+// a softmax weight's log2 and a V scale's exponent, so that the largest weight is
+// 2^z to 2^(z+1); at most 16 + 121, and NaN where every weight is (any power will do).
+// The sum with 1.5 * 2^23 rounds z to an integer and holds it in its low bits.
+__device__ __forceinline__ void scale_of_weights(float z, float &f, float &inv)
+{
+    const uint32_t e = __float_as_uint(__fadd_rn(fmaxf(z, -110.0f), 12582912.0f));
+    const uint32_t bits = (uint32_t(13 + 127) << 23) - (e << 23);
+    f = __uint_as_float(bits);
+    inv = __uint_as_float((uint32_t(2 * 127) << 23) - bits);
+}
+
+constexpr int kLag = 8;     // log2 of the largest softmax weight (16 where the scores' own rounding is that coarse)
 
 // CTAs per SM that the registers and the ring leave room for.
 template <int D, int HS>
@@ -360,18 +374,15 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
         }
         return blk;
     };
-    // ... then its scales, the V scales of a step's 4 groups brought to a common power of two
+    // ... then its scales
     auto load_scales = [&](int blk) {
         return blk >= 0 ? __ldg(reinterpret_cast<const float2 *>(a.scales) + int64_t(blk) * a.kv_heads + kvh)
                         : make_float2(0.0f, 0.0f);
     };
     auto store_meta = [&](int blk, float2 sc) {
-        uint32_t top = __float_as_uint(sc.y) & 0x7fffffffu;
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        float f, inv;
-        scale_to<kVTop>(top, f, inv);
-        sm.meta[tid] = make_float4(sc.x, sc.y * f, inv, blk != -1 ? 0.0f : -INFINITY);
+        const uint32_t bits = __float_as_uint(sc.y) & 0x7fffffffu;
+        const float e = bits == 0 ? -INFINITY : float(int(bits >> 23) - 127);
+        sm.meta[tid] = make_float4(sc.x, sc.y, e, blk != -1 ? 0.0f : -INFINITY);
     };
     const unsigned char *codes = a.codes + int64_t(kvh) * (8 * D) + lane * 16;  // this lane's first piece of block 0
     const int64_t blk_bytes = int64_t(a.kv_heads) * (8 * D);
@@ -441,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
 #pragma unroll
         for (int o = 1; o < kQThreads; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         float f, inv;
-        scale_to<kQTop>(top, f, inv);
+        scale_of_q(top, f, inv);
         if (h >= 8 * HS) continue;  // (d = 64: more threads than heads need)
         uint32_t hi[4], lo[4];
         split2(make_float2(x.x * f, x.y * f), hi[0], lo[0]);
@@ -577,13 +588,18 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
             // 2^kLag, so that the accumulators are rescaled a few times in a row and
             // not at almost every step; weights stay below 2^kLag.
             uint32_t ph[HS][2], pl[HS][2];
-            float mc[HS];
+            // zm: the largest log2 of a weight plus exponent of a V scale, as m_run stands
+            float xl[HS], mc[HS], zm[HS], winv[HS];
             bool passed = false;
+            auto reference = [&](int s) { return m_run[s] == -INFINITY ? 0.0f : m_run[s]; };
 #pragma unroll
             for (int s = 0; s < HS; ++s) {
-                mc[s] = fmaxf(fmaxf(x[s][0].x, x[s][0].y), fmaxf(x[s][1].x, x[s][1].y));
-                mc[s] = fmaxf(mc[s], __shfl_xor_sync(0xffffffffu, mc[s], 1));
+                xl[s] = fmaxf(fmaxf(x[s][0].x, x[s][0].y), fmaxf(x[s][1].x, x[s][1].y));
+                mc[s] = fmaxf(xl[s], __shfl_xor_sync(0xffffffffu, xl[s], 1));
+                zm[s] = (xl[s] - reference(s)) + meta.z;
+                zm[s] = fmaxf(zm[s], __shfl_xor_sync(0xffffffffu, zm[s], 1));
                 mc[s] = fmaxf(mc[s], __shfl_xor_sync(0xffffffffu, mc[s], 2));
+                zm[s] = fmaxf(zm[s], __shfl_xor_sync(0xffffffffu, zm[s], 2));
                 passed = passed || mc[s] > m_run[s] + float(kLag);
             }
             if (__any_sync(0xffffffffu, passed)) {
@@ -592,6 +608,9 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                     if (!(mc[s] > m_run[s] + float(kLag))) mc[s] = m_run[s];
                     const float alpha = mc[s] == -INFINITY ? 1.0f : ex2(m_run[s] - mc[s]);
                     m_run[s] = mc[s];
+                    zm[s] = (xl[s] - reference(s)) + meta.z;
+                    zm[s] = fmaxf(zm[s], __shfl_xor_sync(0xffffffffu, zm[s], 1));
+                    zm[s] = fmaxf(zm[s], __shfl_xor_sync(0xffffffffu, zm[s], 2));
                     l_run[s] *= alpha;
 #pragma unroll
                     for (int j = 0; j < kVC; ++j)
@@ -601,7 +620,9 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
             }
 #pragma unroll
             for (int s = 0; s < HS; ++s) {
-                const float ms = m_run[s] == -INFINITY ? 0.0f : m_run[s];
+                const float ms = reference(s);
+                float f;
+                scale_of_weights(zm[s], f, winv[s]);
                 float2 p[2];
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -610,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                 }
                 const float gs = (p[0].x + p[0].y) + (p[1].x + p[1].y);
                 l_run[s] += gs;
-                split2(mul2(p[0], meta.y), ph[s][0], pl[s][0]);
-                split2(mul2(p[1], meta.y), ph[s][1], pl[s][1]);
+                split2(mul2(mul2(p[0], meta.y), f), ph[s][0], pl[s][0]);
+                split2(mul2(mul2(p[1], meta.y), f), ph[s][1], pl[s][1]);
                 const int h = hl + 8 * s;
                 if (a.mass != nullptr && h < gq) {
                     const int64_t hb = int64_t(b) * a.q_heads + h0 + h;
@@ -637,11 +658,11 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                     float c[4];
                     mma16816_first(c, pa, b0, b1);
                     if constexpr (HS == 1) {
-                        acc[0][j][u] = fma2(add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])), meta.z, acc[0][j][u]);
+                        acc[0][j][u] = fma2(add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])), winv[0], acc[0][j][u]);
                     } else {
                         mma16816(c, pb, b0, b1);
-                        acc[0][j][u] = fma2(make_float2(c[0], c[1]), meta.z, acc[0][j][u]);
-                        acc[HS - 1][j][u] = fma2(make_float2(c[2], c[3]), meta.z, acc[HS - 1][j][u]);
+                        acc[0][j][u] = fma2(make_float2(c[0], c[1]), winv[0], acc[0][j][u]);
+                        acc[HS - 1][j][u] = fma2(make_float2(c[2], c[3]), winv[HS - 1], acc[HS - 1][j][u]);
                     }
                 }
             }
