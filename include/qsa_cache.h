@@ -57,7 +57,8 @@ typedef struct {
  * block_map[block_offset[b] + g], per KV head and for K and V apart:
  *   s = max |x| * r  (r = 1/448 for e4m3, 1/127 for int8, rounded to binary32;
  *   over 4 tokens x d),   code = round_to_nearest_even(x / s),
- * product and quotient binary32, correctly rounded.  A scale below the smallest
+ * product and quotient binary32, correctly rounded (an e4m3 code of a negative
+ * value that rounds to zero, or of -0, is -0: 0x80).  A scale below the smallest
  * normal float is stored as 0 with codes 0 (the group is flushed to zero); a
  * group with a value that is not finite gets the scale NaN and codes 0.
  * Afterwards nothing here reads those f32 rows again: their slots may be

@@ -1,6 +1,6 @@
 """Where the numbers of the coded cache are hardest to keep, against the plain forms
 in 64 bits (tests/cache_helpers.py): scores that leave binary32 or come near, values of
-neighbouring groups whose sizes differ."""
+neighbouring groups whose sizes differ, zeros with a sign."""
 import numpy as np
 import pytest
 
@@ -190,3 +190,45 @@ def test_scores_near_two_to_the_27(q_heads, kv, d, fmt, whole):
         v = V[:, hd // (q_heads // kv)].reshape(-1, d)
         slack = 30 * 2.0 ** -22 * np.abs(v).max()
         assert (out[0, hd] <= v.max(axis=0) + slack).all() and (out[0, hd] >= v.min(axis=0) - slack).all()
+
+
+# ---- zeros with a sign --------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", [ch.E4M3, ch.INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_code_bytes_equal_the_definition_with_signed_zeros(fmt, d):
+    """The bytes, not the numbers they stand for: an e4m3 code has the sign of its value,
+    -0 and what rounds to it included, whatever the group's scale (scales on both sides
+    of 2^-90, below which the quotient is computed in another way)."""
+    need_gpu()
+    r = np.random.RandomState(7)
+    exponents = [-140, -126, -100, -92, -91, -90, -89, -88, -60, -1, 0, 1, 60, 120]
+    h = ch.History([4 * len(exponents)], q_heads=2, kv_heads=2, head_dim=d, fmt=fmt, seed=8)
+    for x in (h.k, h.v):
+        small = r.rand(*x.shape)
+        x[small < 0.3] = 0.0
+        x[small < 0.2] *= np.float32(1e-30)
+        x[(small > 0.3) & (small < 0.4)] *= np.float32(1e-4)
+        x[(small > 0.4) & (small < 0.5)] *= np.float32(1e-36)
+        x *= np.repeat(2.0 ** np.array(exponents) * ch.QMAX[fmt], 4)[:, None, None].astype(np.float64) / 8
+        x[r.rand(*x.shape) < 0.5] *= -1
+    assert np.signbit(h.k[h.k == 0]).any() and not np.signbit(h.k[h.k == 0]).all()
+    _set_cache(h)
+    t = ch.device(h)
+    t["codes"].fill_(0x5a)
+    ch.fill_cache(h, t)
+    raw = t["codes"].cpu().numpy()[h.block_map]
+    n = len(exponents)
+    k = raw[:, :, :4 * d].reshape(n, 2, d // 64, 4, 64).transpose(0, 1, 3, 2, 4).reshape(n, 2, 4, d)
+    v = raw[:, :, 4 * d:].reshape(n, 2, d, 4).transpose(0, 1, 3, 2)
+    table = ch.e4m3_table()[:0x7f]
+    for src, got in ((h.k, k), (h.v, v)):
+        x = src.reshape(n, 4, 2, d).transpose(0, 2, 1, 3)
+        c, s = ch.encode(x, fmt)
+        if fmt == ch.INT8:
+            want = c.astype(np.int8).view(np.uint8)
+        else:
+            want = np.searchsorted(table, np.abs(c)).astype(np.uint8)
+            assert np.array_equal(table[want], np.abs(c))
+            want = np.where(np.signbit(x) & (s > 0)[..., None, None], want | 0x80, want)
+        assert np.array_equal(got, want)

@@ -34,12 +34,15 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c)
 // System/6000, 1990), one more correction by the exact remainder rounds as the
 // division does.  A remainder is exact while it does not underflow: the caller
 // divides where the scale is below 2^-90 (and a quotient so small that its own
-// remainder underflows is far below half the smallest code).
+// remainder underflows is far below half the smallest code).  Of x = -0 the corrections
+// make +0; an e4m3 code holds the sign, so there it is x's, as a division's is.
+template <bool kInt8>
 __device__ __forceinline__ float quotient(float x, float s, float r)
 {
     float q = __fmul_rn(x, r);
     q = __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
-    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+    q = __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+    return kInt8 ? q : copysignf(q, x);
 }
 
 // Four quotients of at most the format's largest code in size, as codes.
@@ -80,8 +83,8 @@ __device__ __forceinline__ void code_rows(const float4 (&r)[4], int l, bool is_k
         const float inv = __frcp_rn(s);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            c[u] = code4<kInt8>(quotient(r[u].x, s, inv), quotient(r[u].y, s, inv), quotient(r[u].z, s, inv),
-                                quotient(r[u].w, s, inv));
+            c[u] = code4<kInt8>(quotient<kInt8>(r[u].x, s, inv), quotient<kInt8>(r[u].y, s, inv),
+                                quotient<kInt8>(r[u].z, s, inv), quotient<kInt8>(r[u].w, s, inv));
     } else if (finite && s > 0.0f) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
