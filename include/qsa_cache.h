@@ -102,7 +102,8 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * += sum over heads h and over the row's tokens t of group g = t/4 of
  * softmax(x)_t, the incomplete last group (g = visible[b]/4) included, so one
  * query adds n_q in all; a row with a score that is NaN makes its groups' weights
- * NaN.  Queries with the same weight_offset share a history:
+ * NaN.  Shares are added to what is there: the caller sets a group's entry to 0
+ * when its first token comes.  Queries with the same weight_offset share a history:
  * their shares are added in a fixed order, so the sum has one value (the rows of
  * different offsets must not overlap).
  *
@@ -176,8 +177,10 @@ typedef struct {
 /* Moves the kept groups of `src` to `dst`, where group kept[b][i] becomes group
  * i, with the raw tail behind them, and sets dst->visible[b] = 4*n_kept[b] +
  * T_b mod 4: raw index keys, pooled keys (in the layout of their new position),
- * slot map, block map and accumulated weights.  The K/V rows and codes do not
- * move: the maps follow them.  kept, n_kept: as qsa_evict_select fills them,
+ * slot map, block map and accumulated weights (of an incomplete last group too;
+ * with T_b mod 4 == 0 entry n_kept[b] is behind the region's end, and the caller's
+ * to set to 0 when the next group starts).  The K/V rows and codes do not move: the
+ * maps follow them.  kept, n_kept: as qsa_evict_select fills them,
  * [B, keep_groups] and [B].  dst's regions hold 4*n_kept[b] + 3 tokens or what
  * the caller knows to be enough, overlap neither each other nor src's; rows
  * behind a region's new end are left as they were.  src->visible and
