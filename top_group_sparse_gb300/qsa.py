@@ -547,6 +547,7 @@ class DeviceBatch:
             raise ValueError("invalid dims")
         # zero-filled: the workspace header must start clean
         self.ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        self.coded_ws = None  # of the calls over a coded cache (make_coded_cache)
         self.step_out, v = _packed([("ids", ((B, self.row_cap), np.int32, -1)),
                                     ("n_ids", ((B,), np.int32, -1)),
                                     ("out", ((B, w.q_heads, w.head_dim), np.float32, float("nan")))], dev)
@@ -780,4 +781,9 @@ class DeviceBatch:
         return qsa_decode_shared(self.dims, self.inputs, self.ids, self.n_ids, self.out, self.ws, stream)
 
     def check_errors(self, stream=None):
-        return qsa_check_errors(self.ws, stream)
+        """(status, flags) of every call on this batch since the last check, those over its coded cache included."""
+        st, flags = qsa_check_errors(self.ws, stream)
+        if self.coded_ws is not None:
+            coded_st, coded_flags = qsa_check_errors(self.coded_ws, stream)
+            st, flags = max(st, coded_st), flags | coded_flags
+        return st, flags
