@@ -187,7 +187,7 @@ qsa_status qsa_attend_coded(const qsa_dims *dims, const qsa_inputs *in, const qs
     const CodedLayout C = make_coded_layout(dims, ids == nullptr, weights != nullptr);
     if ((st = check_ws(ws, ws_bytes, C.total)) != QSA_OK) return st;
     const AttendCodedArgs a = attend_args(dims, in, cache, ids, n_ids, out, weights, weight_offset, ws, C);
-    return from_cuda(launch_attend_coded(a, static_cast<cudaStream_t>(stream), true));
+    return from_cuda(launch_attend_coded(a, static_cast<cudaStream_t>(stream)));
 }
 
 qsa_status qsa_decode_coded(const qsa_dims *dims, const qsa_inputs *in, const qsa_coded_cache *cache,
@@ -212,7 +212,7 @@ qsa_status qsa_decode_coded(const qsa_dims *dims, const qsa_inputs *in, const qs
                                     out, weights, weight_offset, ws, C);
     a.ids_out = ids;
     a.n_ids_out = n_ids;
-    return from_cuda(launch_attend_coded(a, s, true));
+    return from_cuda(launch_attend_coded(a, s));
 }
 
 qsa_status qsa_evict_select(const qsa_dims *dims, const int32_t *visible, const float *weights,

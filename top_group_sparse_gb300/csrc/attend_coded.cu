@@ -727,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
 }
 
 template <int D, int HS, bool kInt8>
-cudaError_t launch_t(const AttendCodedArgs &a, int runs, cudaStream_t s, bool pdl)
+cudaError_t launch_t(const AttendCodedArgs &a, int runs, cudaStream_t s)
 {
     const size_t smem = sizeof(Sm<D, HS>);
     static bool attr_done[64] = {};
@@ -741,7 +741,7 @@ cudaError_t launch_t(const AttendCodedArgs &a, int runs, cudaStream_t s, bool pd
         attr_done[dev] = true;
     }
     return launch_kernel(attend_coded_kernel<D, HS, kInt8>, dim3(unsigned(runs + (a.sharing != nullptr ? 2 : 1)), unsigned(a.kv_heads), unsigned(a.batch)),
-                         dim3(kThreads), smem, s, pdl, a);
+                         dim3(kThreads), smem, s, true, a);
 }
 
 static_assert(sizeof(Sm<128, 2>) <= 227 * 1024, "shared memory per CTA");
@@ -758,7 +758,7 @@ bool attend_coded_shape_supported(int head_dim, int q_heads, int kv_heads)
     return (head_dim == 64 || head_dim == 128) && q_heads / kv_heads <= kMaxGqa && kv_heads <= 65535;
 }
 
-cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s, bool pdl)
+cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s)
 {
     if (a.batch == 0) return cudaSuccess;
     const bool whole = a.ids == nullptr;
@@ -767,11 +767,11 @@ cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s, bool p
     const bool one = a.q_heads / a.kv_heads <= 8, i8 = a.format == QSA_CODE_INT8;
     cudaError_t e;
     if (a.head_dim == 128)
-        e = one ? (i8 ? launch_t<128, 1, true>(a, runs, s, pdl) : launch_t<128, 1, false>(a, runs, s, pdl))
-                : (i8 ? launch_t<128, 2, true>(a, runs, s, pdl) : launch_t<128, 2, false>(a, runs, s, pdl));
+        e = one ? (i8 ? launch_t<128, 1, true>(a, runs, s) : launch_t<128, 1, false>(a, runs, s))
+                : (i8 ? launch_t<128, 2, true>(a, runs, s) : launch_t<128, 2, false>(a, runs, s));
     else
-        e = one ? (i8 ? launch_t<64, 1, true>(a, runs, s, pdl) : launch_t<64, 1, false>(a, runs, s, pdl))
-                : (i8 ? launch_t<64, 2, true>(a, runs, s, pdl) : launch_t<64, 2, false>(a, runs, s, pdl));
+        e = one ? (i8 ? launch_t<64, 1, true>(a, runs, s) : launch_t<64, 1, false>(a, runs, s))
+                : (i8 ? launch_t<64, 2, true>(a, runs, s) : launch_t<64, 2, false>(a, runs, s));
     if (e != cudaSuccess) return e;
     return launch_merge_coded(a, s);
 }

@@ -111,7 +111,7 @@ struct AttendCodedArgs {
 };
 bool attend_coded_shape_supported(int head_dim, int q_heads, int kv_heads);
 cudaError_t launch_merge_coded(const AttendCodedArgs &a, cudaStream_t s);  // after the runs' states
-cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s, bool pdl);
+cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s);
 
 struct EvictSelectArgs {
     const int32_t *visible;
