@@ -34,7 +34,7 @@ constexpr int kCluster = 8;
 constexpr int kOneCta = 4096;               // histories of up to so many groups: one CTA, no cluster
 
 struct SelectSmem {
-    alignas(16) uint32_t hist[3 * kBins];   // kBins per pass: a pass needs no barrier behind the others' reads
+    alignas(16) uint32_t hist[3][kBins];    // one per pass: a pass needs no barrier behind the others' reads
     uint32_t warp_sum[2][kWarps];           // by turns: a scan needs one barrier
     uint32_t bin, rest, equal;
 };
@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
     }
     auto key_at = [&](int i) { return in_smem ? keys[i] : weight_key(__ldg(w + s0 + i)); };
 #pragma unroll
-    for (int i = 0; i < 3 * kBins / kThreads; ++i) sm.hist[tid + i * kThreads] = 0;
+    for (int i = 0; i < kBins / kThreads; ++i)
+        for (auto &counts : sm.hist) counts[tid + i * kThreads] = 0;
     __syncthreads();
 
     // ---- K, the need-th largest key, and how many keys equal to it are kept; the keys
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictSelec
         int shift = 21, bits = 11;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            uint32_t *my_hist = sm.hist + pass * kBins;
+            uint32_t *my_hist = sm.hist[pass];
             const uint32_t above_mask = pass == 0 ? 0u : 0xffffffffu << (shift + bits);
 #pragma unroll 4
             for (int i0 = 0; i0 < sn; i0 += kThreads) {
