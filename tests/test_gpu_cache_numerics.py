@@ -1,6 +1,6 @@
 """Where the numbers of the coded cache are hardest to keep, against the plain forms
 in 64 bits (tests/cache_helpers.py): scores that leave binary32 or come near, values of
-neighbouring groups whose sizes differ, zeros with a sign."""
+neighbouring groups whose sizes differ, zeros with a sign, long shared sums."""
 import numpy as np
 import pytest
 
@@ -232,3 +232,20 @@ def test_code_bytes_equal_the_definition_with_signed_zeros(fmt, d):
             assert np.array_equal(table[want], np.abs(c))
             want = np.where(np.signbit(x) & (s > 0)[..., None, None], want | 0x80, want)
         assert np.array_equal(got, want)
+
+
+# ---- several queries of one long history ----------------------------------------------------
+
+@pytest.mark.parametrize("fmt,q_heads,kv,d", [(ch.E4M3, 8, 2, 64), (ch.INT8, 16, 1, 128)])
+def test_queries_of_one_long_history_over_all_of_it(fmt, q_heads, kv, d):
+    """Five queries of one history on both sides of the changes of the run length, with
+    the weights they add to its accumulators."""
+    need_gpu()
+    visible = [4 * 1024 + 3, 4 * 1025, 4 * 4096 + 1, 4 * 4097 + 2, 4 * 4400 + 3]
+    h = ch.History(visible, q_heads=q_heads, kv_heads=kv, head_dim=d, fmt=fmt, seed=11, shared=True)
+    out, got, flags = _attend(h, None, weights=True)
+    assert flags == 0
+    ref, share, tol, rel = ch.attention(h)
+    assert (np.abs(out - ref).max(axis=(1, 2)) <= tol).all()
+    w, wt = ch.add_weights(h, share, rel)
+    assert (np.abs(got - w) <= wt).all(), np.abs(got - w).max()

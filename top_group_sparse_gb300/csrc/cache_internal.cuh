@@ -19,8 +19,9 @@ namespace qsa {
 // groups, 16 / 2 heads x 128: runs of 64 107, of 128 96; 32 ragged rows of up to
 // 16,384 groups: runs of 128 95, of 256 84.  4 rows of 10,000 groups with 16 heads on
 // one: 128 19, 256 27.  Selected rows (at most 512 groups): 128 queries 45, 35, 31 with
-// runs of 32, 64, 128; 8 queries 5.1, 5.3, 7.2.  Beyond 131,072 groups the length
-// doubles so that a row has at most 512 runs.
+// runs of 32, 64, 128; 8 queries 5.1, 5.3, 7.2.  Beyond 131,072 groups (65,536 with 9
+// to 16 heads per KV head, whose runs are half as long) the length doubles so that a
+// row has at most 512 runs.
 constexpr int kCodedRunRows = 64;
 
 __host__ __device__ inline int coded_run_groups(int groups, bool whole, int heads_per_kv)
