@@ -38,11 +38,11 @@
 // and the query are three dependent loads -- and ends.
 //
 // Bound: 8*d + 8 bytes per (group, KV head), read once.  8 histories of 262,144
-// tokens (16 / 2 heads x 128, e4m3, 1.08 GB): 178 us of this kernel, 6.1 TB/s, the
+// tokens (16 / 2 heads x 128, e4m3, 1.08 GB): 179 us of this kernel, 6.1 TB/s, the
 // tensor pipe 25-30 % and the issue slots about half busy; with the blocks in
 // order instead of permuted 7 % less, the rest of the distance to the copy rate
 // (6.77 TB/s) being starts and ends.  Rows of a few thousand tokens and selected
-// rows (512 groups: 5.3 us for 8 queries) are bound by a CTA's start and end.
+// rows (512 groups: 5.4 us for 8 queries) are bound by a CTA's start and end.
 // Tried and not kept: a ring of three (189 us), copies by the bulk engine (its
 // operands are uniform, so four lanes' copies are issued one after the other:
 // 60 more instructions a step, 188 us), resident CTAs that take several runs with
