@@ -107,8 +107,8 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * their shares are added in a fixed order, so the sum has one value (the rows of
  * different offsets must not overlap).
  *
- * The codes are exact in 16-bit floats; q and the softmax weights (times their
- * group's V scale) enter the matrix products as a sum of two 16-bit floats each:
+ * The codes are exact in 16-bit floats; q and the softmax weights (each times its
+ * group's V scale, in binary32) enter the products as a sum of two 16-bit floats:
  * to 2^-22 of themselves, or 2^-37 of the largest of the head's q, of the head's
  * weights in four consecutive groups of the row, where that is more.  All sums,
  * maxima and outputs are binary32.  Two products have to stay below 2^128 for
