@@ -559,7 +559,7 @@ def _plan(s):
                                      **{k: s[k] for k in ("q_norm", "k_norm", "q_idx_norm", "idx_key_norm")})
         return {"qsa": qsa, "dims": dims, "tokens": tokens,
                 "inputs": qsa.QsaInputs(num_slots=s["k_cache"].shape[0], key_offset=at["slot_offset"], **at),
-                "ws": torch.zeros(qsa.qsa_workspace_size(dims), dtype=torch.uint8, device=DEV)}
+                "ws": torch.zeros(qsa.QSA_ROWS_WORKSPACE_BYTES, dtype=torch.uint8, device=DEV)}
     dims = qsa.make_dims(c["batch"], 8, 64, c.get("heads", c["kv"]), c["kv"], c["d"], budget_groups=c.get("rows") or 512,
                          max_visible=max(_lengths(c)))
     cache = qsa.QsaCodedCache.of(s["codes"], s["scales"], s["block_map"], s["block_offset"], FORMAT[c["fmt"]])
