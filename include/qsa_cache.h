@@ -1,5 +1,5 @@
 /*
- * qsa_cache.h -- bounded caches for long decodes: K/V rows held in 8 bits, the
+ * qsa_cache.h -- bounded caches for long decodes: K/V rows held in 8 or 4 bits, the
  * attention that reads them, and the eviction of groups by the attention that
  * they have received.  Part of libqsa; the conventions of qsa.h hold for every
  * call here (device pointers of the current device, the caller owns every
@@ -29,6 +29,8 @@ extern "C" {
 
 #define QSA_CODE_E4M3 0 /* 8-bit float, 4 exponent and 3 mantissa bits, largest value 448 */
 #define QSA_CODE_INT8 1 /* signed integer, -127 .. 127                                    */
+#define QSA_CODE_E2M1 4 /* 4-bit float, 2 exponent and 1 mantissa bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6, and negative */
+#define QSA_CODE_INT4 5 /* 4-bit integer, -7 .. 7, stored as 1 .. 15                      */
 
 /* K and V of complete groups, one block per group, by PHYSICAL block number.
  * A code c of K in block p and KV head h stands for scales[p][h][0] * c, one
@@ -39,15 +41,29 @@ extern "C" {
  * side by side and two tokens fill the 128 bytes that shared memory serves at
  * once; V: the four tokens of one dim are the operand word of the second
  * product).  A scale is finite, or NaN for a group that held a value that is
- * not finite: every output that attends to such a group is NaN. */
+ * not finite: every output that attends to such a group is NaN.
+ *
+ * In 4 bits each tile of four tokens by four neighbouring dims (4r .. 4r+3) has a scale
+ * of its own besides, an e4m3 number t >= 0, and a code c stands for scales[p][h][.] * t * c:
+ * 4.5 bits a value.  Layout of a (block, head), 9*d/2 bytes; a word is 32 bits, least
+ * significant byte first, and holds four pairs of codes p = 0 .. 3 -- for e2m1 in the low and
+ * the high half of byte p, for int4 in bits 4p .. 4p+3 and 4p+16 .. 4p+19, as code + 8:
+ *   K: [d/64 j][2 i][4 c][2 t][2 w] words at byte 128*j + 64*i + 16*c + 8*t + 4*w: pair p of
+ *      token 2t + i is dims 64j + 16c + 8w + p and + 4
+ *   V: [d/64 m][8 h][2 n][2 w] words at byte 2*d + 128*m + 16*h + 8*n + 4*w: pair p of dim
+ *      64m + 32n + 4h + 2w + p/2 is tokens 2(p%2) and + 1
+ *   tile scales of K at byte 4*d: that of dims 64j + 16c + 4r .. at c*d/16 + 4j + r
+ *   tile scales of V at byte 4*d + d/4: that of dims 64m + 32n + 4h .. at h*d/32 + 2m + n
+ * (what a lane of the attention's products holds sits side by side, and the two codes of a
+ * pair are the two halves of one of its operand registers). */
 typedef struct {
-    uint8_t *codes;              /* [num_blocks, n_kv, 8*d], 16-byte aligned               */
+    uint8_t *codes;              /* [num_blocks, n_kv, 8*d], or 9*d/2 in 4 bits; 16-byte aligned */
     float *scales;               /* [num_blocks, n_kv, 2], 16-byte aligned                 */
     int64_t num_blocks;
     const int32_t *block_map;    /* logical -> physical: group g of query b is in block    */
                                  /*   block_map[block_offset[b] + g]                       */
     const int64_t *block_offset; /* [B] first block-map entry of query b's history         */
-    int32_t format;              /* QSA_CODE_E4M3 or QSA_CODE_INT8                         */
+    int32_t format;              /* QSA_CODE_E4M3, _INT8, _E2M1 or _INT4                   */
 } qsa_coded_cache;
 
 /* Codes complete groups: for each query b and g in [group_begin[b],
@@ -61,6 +77,13 @@ typedef struct {
  * value that rounds to zero, or of -0, is -0: 0x80).  A scale below the smallest
  * normal float is stored as 0 with codes 0 (the group is flushed to zero); a
  * group with a value that is not finite gets the scale NaN and codes 0.
+ * In 4 bits, with c = 6 (e2m1) or 7 (int4), per KV head and for K and V apart:
+ *   s = max |x| * rn(1 / (448 c)) over 4 tokens x d, flushed as above (then with tile scales 0);
+ *   t = e4m3(min(448, a / (c s))) of each tile, a = max |x| over its 16 values;
+ *   code = round_to_nearest_even(x / (t s)), at most c in size, or 0 where t = 0,
+ * every product and quotient binary32, correctly rounded, t to the nearest e4m3 number (even
+ * on ties; a tile below about 2^-19 of the group's largest value gets 0), codes to the nearest
+ * number of their format (the one with an even last bit on ties).
  * Afterwards nothing here reads those f32 rows again: their slots may be
  * reused (a later tail's, for instance).  max_groups (host) bounds group_end[b]
  * - group_begin[b] for every b and sizes the launch: a decode step that
@@ -107,7 +130,7 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * their shares are added in a fixed order, so the sum has one value (the rows of
  * different offsets must not overlap).
  *
- * The codes are exact in 16-bit floats; q and the softmax weights (each times its
+ * The codes, in 4 bits times their tile scales, are exact in 16-bit floats; q and the softmax weights (each times its
  * group's V scale, in binary32) enter the products as a sum of two 16-bit floats:
  * to 2^-22 of themselves, or 2^-37 of the largest of the head's q, of the head's
  * weights in four consecutive groups of the row, where that is more.  All sums,

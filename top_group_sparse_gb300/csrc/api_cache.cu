@@ -48,23 +48,8 @@ CodedLayout make_coded_layout(const qsa_dims *d, bool whole, bool weights)
     return C;
 }
 
-namespace {
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool given(const void *p, size_t a) { return p != nullptr && aligned(p, a); }
-qsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
-
-template <typename T>
-T *at(void *ws, size_t off)
-{
-    return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + off);
-}
-
-qsa_status check_ws(void *ws, size_t ws_bytes, size_t need)
-{
-    if (!given(ws, kWsAlign)) return QSA_ERR_INVALID_ARG;
-    return ws_bytes < need ? QSA_ERR_WORKSPACE_TOO_SMALL : QSA_OK;
-}
+static bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+static bool given(const void *p, size_t a) { return p != nullptr && aligned(p, a); }
 
 // The f32 cache behind the slot map.
 qsa_status check_rows(const qsa_inputs *in)
@@ -80,8 +65,23 @@ qsa_status check_cache(const qsa_coded_cache *c)
     if (!c || !given(c->codes, 16) || !given(c->scales, 16) || !given(c->block_map, 4) || !given(c->block_offset, 8) ||
         c->num_blocks < 0)
         return QSA_ERR_INVALID_ARG;
-    if (c->format != QSA_CODE_E4M3 && c->format != QSA_CODE_INT8) return QSA_ERR_INVALID_ARG;
-    return QSA_OK;
+    return format_known(c->format) ? QSA_OK : QSA_ERR_INVALID_ARG;
+}
+
+namespace {
+
+qsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
+
+template <typename T>
+T *at(void *ws, size_t off)
+{
+    return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + off);
+}
+
+qsa_status check_ws(void *ws, size_t ws_bytes, size_t need)
+{
+    if (!given(ws, kWsAlign)) return QSA_ERR_INVALID_ARG;
+    return ws_bytes < need ? QSA_ERR_WORKSPACE_TOO_SMALL : QSA_OK;
 }
 
 qsa_status check_attend(const qsa_dims *d, const qsa_inputs *in, const qsa_coded_cache *cache, const float *out,

@@ -1,9 +1,11 @@
 // cache_internal.cuh -- internal declarations of the coded cache, the attention
-// over it and the eviction (include/qsa_cache.h).
+// over it and the eviction (include/qsa_cache.h), and of the rows on their way into
+// the caches and back (include/qsa_rows.h).
 #pragma once
 
 #include "qsa_cache.h"
 #include "qsa_internal.cuh"
+#include "qsa_rows.h"
 
 namespace qsa {
 
@@ -84,6 +86,40 @@ struct CodeArgs {
     uint32_t *err;
 };
 cudaError_t launch_code_groups(const CodeArgs &a, cudaStream_t s);
+// The way back: codes and scales are read, k_cache and v_cache written.
+cudaError_t launch_read_groups(const CodeArgs &a, cudaStream_t s);
+
+// Bytes of one (group, KV head)'s codes; in 4 bits with their tile scales.
+__host__ __device__ constexpr bool is_4bit(int format) { return format == QSA_CODE_E2M1 || format == QSA_CODE_INT4; }
+__host__ __device__ constexpr int code_bytes(int format, int d) { return is_4bit(format) ? 9 * d / 2 : 8 * d; }
+inline bool format_known(int f)
+{
+    return f == QSA_CODE_E4M3 || f == QSA_CODE_INT8 || f == QSA_CODE_E2M1 || f == QSA_CODE_INT4;
+}
+
+// Heads of one width that a new token brings: q, k and v, or q_idx and idx_key.
+struct AppendFamily {
+    const void *rows[3];
+    int64_t stride[3];
+    const float *norm[3];
+    float *out[3];          // [0]: a row per query; the others: by slot, or by logical row
+    int32_t heads[3];       // 0: not given
+    int32_t out_heads;      // heads of a row of out[1], out[2]
+    int32_t any_norm, dims, neighbours;
+    const float *freq;
+    int32_t all_heads, steps, tasks;  // the launcher's: a step is 128/width heads, a task some steps
+};
+struct AppendArgs {
+    AppendFamily family[2];
+    const int32_t *positions, *visible, *slot_map;
+    const int64_t *slot_offset, *key_offset;
+    int64_t num_slots;
+    float eps;
+    int32_t axes, batch, max_visible;
+    int32_t steps, tasks;   // the launcher's: steps of a task, tasks of a token
+    uint32_t *err;
+};
+cudaError_t launch_append(AppendArgs a, int type, int head_dim, int idx_dim, int num_sms, cudaStream_t s);
 
 struct AttendCodedArgs {
     const float *q;
@@ -113,6 +149,7 @@ struct AttendCodedArgs {
 bool attend_coded_shape_supported(int head_dim, int q_heads, int kv_heads);
 cudaError_t launch_merge_coded(const AttendCodedArgs &a, cudaStream_t s);  // after the runs' states
 cudaError_t launch_attend_coded(const AttendCodedArgs &a, cudaStream_t s);
+cudaError_t launch_attend_coded4(const AttendCodedArgs &a, int runs, cudaStream_t s);  // the runs alone, 4-bit formats
 
 struct EvictSelectArgs {
     const int32_t *visible;
@@ -137,6 +174,9 @@ cudaError_t launch_evict_compact(const EvictCompactArgs &a, int num_sms, cudaStr
 qsa_status score_and_select(const qsa_dims *d, const qsa_inputs *in, const float *pooled, const int64_t *pool_offset,
                             void *ws, const Layout &L, cudaStream_t s);
 int num_sms_of_current_device();
+// api_cache.cu: the f32 cache behind the slot map, and a coded cache, as arguments.
+qsa_status check_rows(const qsa_inputs *in);
+qsa_status check_cache(const qsa_coded_cache *c);
 
 // ---- device helpers ----------------------------------------------------------
 

@@ -1,5 +1,6 @@
-// coded.cu -- complete groups' K/V rows turned into 8-bit codes with a scale
-// per (group, KV head), for K and for V (include/qsa_cache.h: qsa_code_groups).
+// coded.cu -- complete groups' K/V rows turned into 8- or 4-bit codes with a scale
+// per (group, KV head), for K and for V (include/qsa_cache.h: qsa_code_groups), and
+// codes turned back into rows (include/qsa_rows.h: qsa_read_groups).
 //
 // s = max|x| * (1/Q) over the group's 4 x d values, code = rn(x / s): each value
 // is off by at most half a step of its code's format.  1/Q is the binary32
@@ -12,6 +13,13 @@
 // leave from one lane, and every load is a 16-byte piece of a row.  25,063 groups
 // x 2 heads x 128: 43 us, 5.9 TB/s; with a division per value (793 instead of
 // about 350 instructions per warp, 60 % of the issue slots) it was 57 us.
+//
+// In 4 bits a lane's 4 x 4 values are one tile, so a tile's scale t never leaves the lane:
+// t = e4m3(a / (c s)) and code = rn(x / (t s)) by the same quotients, t s being normal and
+// above 2^-90 where s is above 2^-80.  A word of K is two tiles of a token, so lanes exchange
+// their halves of it with their neighbours; a tile of V is 8 bytes of one lane.
+#include <cuda_fp16.h>
+
 #include "cache_internal.cuh"
 
 namespace qsa {
@@ -104,7 +112,128 @@ __device__ __forceinline__ void code_rows(const float4 (&r)[4], int l, bool is_k
     }
 }
 
-template <int D, bool kInt8>
+// Two codes of 4 bits, |x| and |y| at most the format's largest (e2m1: more saturates), as
+// the low and the high half of a byte (e2m1), or x's code + 8 in the low four bits (int4).
+__device__ __forceinline__ uint32_t nibbles_int4(float x)
+{
+    return __float_as_uint(__fadd_rn(x, 12582912.0f + 8.0f)) & 15u;  // as in code4; 8 is even
+}
+__device__ __forceinline__ uint32_t bytes_e2m1(float2 a, float2 b, float2 c, float2 d)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+    return r;
+}
+
+// An e4m3 number from its code, and the code of the number nearest to x >= 0.
+__device__ __forceinline__ float from_e4m3(uint32_t code)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(code)));
+    return __half2float(__ushort_as_half(uint16_t(h)));
+}
+__device__ __forceinline__ uint32_t to_e4m3(float x)
+{
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(x));
+    return c & 0xffu;
+}
+
+// code_rows in 4 bits: this lane's dims are one tile.
+template <int D, bool kInt4>
+__device__ __forceinline__ void code_rows4(const float4 (&r)[4], int l, bool is_k, uint8_t *dst, float *scale_dst)
+{
+    constexpr float kTop = kInt4 ? 7.0f : 6.0f;
+    float most = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) most = max_abs3(max_abs3(most, r[u].x, r[u].y), r[u].z, r[u].w);
+    uint32_t bits = __float_as_uint(most);
+#pragma unroll
+    for (int o = D / 8; o > 0; o >>= 1) bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, o));
+    const bool finite = bits < 0x7f800000u;
+    float s = __fmul_rn(__uint_as_float(bits), kInt4 ? 1.0f / 3136.0f : 1.0f / 2688.0f);
+    if (s < 1.17549435e-38f) s = 0.0f;
+    float y[4][4];  // [token][dim]
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u][0] = r[u].x, y[u][1] = r[u].y, y[u][2] = r[u].z, y[u][3] = r[u].w;
+    uint32_t tile = 0;
+    if (finite && s > 0.0f) {
+        const float unit = __fmul_rn(kTop, s);
+        const bool fast = s > 0x1p-80f;
+        tile = to_e4m3(fast ? quotient<true>(most, unit, __frcp_rn(unit)) : __fdiv_rn(most, unit));
+        const float ts = __fmul_rn(from_e4m3(tile), s);
+        if (fast) {
+            const float inv = __frcp_rn(ts);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[u][j] = quotient<kInt4>(y[u][j], ts, inv);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[u][j] = __fdiv_rn(y[u][j], ts);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[u][j] = tile != 0 ? fminf(fmaxf(y[u][j], -kTop), kTop) : 0.0f;
+    if (l == 0) *scale_dst = finite ? s : __int_as_float(0x7fffffff);
+    if (is_k) {
+        const int j = l / 16, c = l % 16 / 4, q = l % 4;  // tile q of dims 64j + 16c ..
+        uint32_t word[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t own;  // this tile's four codes of token u, where the word's first tile has them
+            if constexpr (kInt4) {
+                own = nibbles_int4(y[u][0]) | nibbles_int4(y[u][1]) << 4 | nibbles_int4(y[u][2]) << 8 | nibbles_int4(y[u][3]) << 12;
+            } else {
+                own = bytes_e2m1(make_float2(y[u][0], 0.f), make_float2(y[u][1], 0.f), make_float2(y[u][2], 0.f), make_float2(y[u][3], 0.f));
+            }
+            constexpr int kSecond = kInt4 ? 16 : 4;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+            word[u] = q % 2 == 0 ? own | other << kSecond : other | own << kSecond;
+        }
+        // of the two words w = q/2 of tokens 2t + i, this lane stores those of t = q%2
+        uint8_t *to = dst + j * 128 + c * 16 + (q % 2) * 8 + (q / 2) * 4;
+        *reinterpret_cast<uint32_t *>(to) = q % 2 == 0 ? word[0] : word[2];
+        *reinterpret_cast<uint32_t *>(to + 64) = q % 2 == 0 ? word[1] : word[3];
+        dst[4 * D + c * (D / 16) + 4 * j + q] = uint8_t(tile);
+    } else {
+        uint32_t word[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            if constexpr (kInt4) {
+                word[w] = 0;
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    word[w] |= nibbles_int4(y[2 * (p % 2)][2 * w + p / 2]) << (4 * p) |
+                               nibbles_int4(y[2 * (p % 2) + 1][2 * w + p / 2]) << (4 * p + 16);
+            } else {
+                word[w] = bytes_e2m1(make_float2(y[0][2 * w], y[1][2 * w]), make_float2(y[2][2 * w], y[3][2 * w]),
+                                     make_float2(y[0][2 * w + 1], y[1][2 * w + 1]), make_float2(y[2][2 * w + 1], y[3][2 * w + 1]));
+            }
+        }
+        const int mn = l / 8, h = l % 8;  // dims 32 mn + 4h ..
+        *reinterpret_cast<uint2 *>(dst + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8) = make_uint2(word[0], word[1]);
+        dst[4 * D + D / 4 + h * (D / 32) + mn] = uint8_t(tile);
+    }
+}
+
+template <int D, int kFormat>
+__device__ __forceinline__ void code_rows_as(const float4 (&r)[4], int l, bool is_k, uint8_t *dst, float *scale_dst)
+{
+    if constexpr (is_4bit(kFormat)) code_rows4<D, kFormat == QSA_CODE_INT4>(r, l, is_k, dst, scale_dst);
+    else code_rows<D, kFormat == QSA_CODE_INT8>(r, l, is_k, dst, scale_dst);
+}
+
+template <int D, int kFormat>
 __global__ void __launch_bounds__(kThreads) code_groups_kernel(const CodeArgs a)
 {
     const int b = blockIdx.y;
@@ -134,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) code_groups_kernel(const CodeArgs a)
         if (!ok && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
         row[u] = ok ? (int64_t(slot) * a.kv_heads + h) * D : -1;
     }
-    uint8_t *dst = a.codes + (int64_t(blk) * a.kv_heads + h) * (8 * D);
+    uint8_t *dst = a.codes + (int64_t(blk) * a.kv_heads + h) * code_bytes(kFormat, D);
     float *sdst = a.scales + (int64_t(blk) * a.kv_heads + h) * 2;
     auto load = [&](const float *cache, int l, float4 (&r)[4]) {
 #pragma unroll
@@ -146,29 +275,175 @@ __global__ void __launch_bounds__(kThreads) code_groups_kernel(const CodeArgs a)
         float4 k[4], v[4];
         load(a.k_cache, lane, k);
         load(a.v_cache, lane, v);
-        code_rows<D, kInt8>(k, lane, true, dst, sdst);
-        code_rows<D, kInt8>(v, lane, false, dst, sdst + 1);
+        code_rows_as<D, kFormat>(k, lane, true, dst, sdst);
+        code_rows_as<D, kFormat>(v, lane, false, dst, sdst + 1);
     } else {                   // lanes 0..15 take K, lanes 16..31 V
         const bool is_k = lane < 16;
         float4 r[4];
         load(is_k ? a.k_cache : a.v_cache, lane & 15, r);
-        code_rows<D, kInt8>(r, lane & 15, is_k, dst, sdst + (is_k ? 0 : 1));
+        code_rows_as<D, kFormat>(r, lane & 15, is_k, dst, sdst + (is_k ? 0 : 1));
     }
+}
+
+// ---- the way back ---------------------------------------------------------------------
+// Values of this lane's dims (4*l .. 4*l+3) of the four tokens of a (group, head), K or V.
+// A product of a code and its tile's scale is exact in binary32.
+
+// Two codes of a byte (e2m1), the low half first.
+__device__ __forceinline__ float2 from_e2m1(uint32_t byte)
+{
+    uint32_t h;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(byte));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+template <int D, bool kInt4>
+__device__ __forceinline__ void read_rows4(const uint8_t *src, int l, bool is_k, float s, float4 (&r)[4])
+{
+    float y[4][4];
+    uint32_t tile;
+    if (is_k) {
+        const int j = l / 16, c = l % 16 / 4, q = l % 4;
+        tile = __ldg(src + 4 * D + c * (D / 16) + 4 * j + q);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint8_t *word = src + j * 128 + (u % 2) * 64 + c * 16 + (u / 2) * 8 + (q / 2) * 4;
+            const uint32_t own = __ldg(reinterpret_cast<const uint32_t *>(word)) >> (q % 2 * (kInt4 ? 16 : 4));
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                y[u][p] = kInt4 ? float(int(own >> (4 * p) & 15u) - 8) : from_e2m1(own >> (8 * p)).x;
+        }
+    } else {
+        const int mn = l / 8, h = l % 8;
+        tile = __ldg(src + 4 * D + D / 4 + h * (D / 32) + mn);
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8));
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint32_t word = w == 0 ? v.x : v.y;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float2 two = kInt4 ? make_float2(float(int(word >> (4 * p) & 15u) - 8), float(int(word >> (4 * p + 16) & 15u) - 8))
+                                         : from_e2m1(word >> (8 * p));
+                y[2 * (p % 2)][2 * w + p / 2] = two.x;
+                y[2 * (p % 2) + 1][2 * w + p / 2] = two.y;
+            }
+        }
+    }
+    const float t = from_e4m3(tile);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) r[u] = make_float4(y[u][0] * t * s, y[u][1] * t * s, y[u][2] * t * s, y[u][3] * t * s);
+}
+
+// The number that byte u of a word of 8-bit codes stands for.
+template <bool kInt8>
+__device__ __forceinline__ float from_byte(uint32_t word, int u)
+{
+    return kInt8 ? float(int8_t(word >> (8 * u))) : from_e4m3(word >> (8 * u) & 0xffu);
+}
+
+template <int D, bool kInt8>
+__device__ __forceinline__ void read_rows8(const uint8_t *src, int l, bool is_k, float s, float4 (&r)[4])
+{
+    if (is_k) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + (l / 16) * 256 + u * 64 + (l % 16) * 4));
+            r[u] = make_float4(from_byte<kInt8>(w, 0) * s, from_byte<kInt8>(w, 1) * s, from_byte<kInt8>(w, 2) * s,
+                               from_byte<kInt8>(w, 3) * s);
+        }
+    } else {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 4 * D + l * 16));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            r[u] = make_float4(from_byte<kInt8>(w.x, u) * s, from_byte<kInt8>(w.y, u) * s, from_byte<kInt8>(w.z, u) * s,
+                               from_byte<kInt8>(w.w, u) * s);
+    }
+}
+
+// Bound by memory, by its stores: a warp takes one (group, head), reads its codes and
+// writes 32*d bytes of rows in whole 16-byte pieces.
+template <int D, int kFormat>
+__global__ void __launch_bounds__(kThreads) read_groups_kernel(const CodeArgs a)
+{
+    const int b = blockIdx.y;
+    const int lane = threadIdx.x & 31;
+    wait_for_predecessor();
+    const int g_begin = __ldg(a.group_begin + b), g_end = __ldg(a.group_end + b);
+    if (g_begin < 0 || g_end < g_begin || g_end > a.g_max || g_end - g_begin > a.max_groups) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, QSA_DEVERR_VISIBLE_RANGE);
+        return;
+    }
+    const int64_t item = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);  // (group, KV head), heads fastest
+    const int64_t gi = item / a.kv_heads;
+    const int h = int(item - gi * a.kv_heads);
+    if (gi >= g_end - g_begin) return;
+    const int64_t g = g_begin + gi;
+    const int blk = __ldg(a.block_map + __ldg(a.block_offset + b) + g);
+    const bool there = blk >= 0 && blk < a.num_blocks;
+    if (!there && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
+    const int32_t *smap = a.slot_map + __ldg(a.slot_offset + b) + 4 * g;
+    int64_t row[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int slot = __ldg(smap + u);
+        const bool ok = slot >= 0 && slot < a.num_slots;
+        if (!ok && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
+        row[u] = ok ? (int64_t(slot) * a.kv_heads + h) * D : -1;
+    }
+    const uint8_t *src = a.codes + (int64_t(blk) * a.kv_heads + h) * code_bytes(kFormat, D);
+    const float *ssrc = a.scales + (int64_t(blk) * a.kv_heads + h) * 2;
+    auto read = [&](int l, bool is_k) {
+        float4 r[4];
+        if (there) {
+            const float s = __ldg(ssrc + (is_k ? 0 : 1));
+            if constexpr (is_4bit(kFormat)) read_rows4<D, kFormat == QSA_CODE_INT4>(src, l, is_k, s, r);
+            else read_rows8<D, kFormat == QSA_CODE_INT8>(src, l, is_k, s, r);
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float *cache = const_cast<float *>(is_k ? a.k_cache : a.v_cache);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (row[u] >= 0) *(reinterpret_cast<float4 *>(cache + row[u]) + l) = r[u];
+    };
+    if constexpr (D == 128) {
+        read(lane, true);
+        read(lane, false);
+    } else {
+        read(lane & 15, lane < 16);
+    }
+}
+
+template <int D>
+cudaError_t launch_d(const CodeArgs &a, bool back, cudaStream_t s)
+{
+    const int64_t blocks = (int64_t(a.max_groups) * a.kv_heads + kWarps - 1) / kWarps;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const dim3 grid(unsigned(blocks), unsigned(a.batch));
+    auto launch = [&](void (*code)(const CodeArgs), void (*read)(const CodeArgs)) {
+        return launch_kernel(back ? read : code, grid, dim3(kThreads), 0, s, true, a);
+    };
+    switch (a.format) {
+        case QSA_CODE_E4M3: return launch(code_groups_kernel<D, QSA_CODE_E4M3>, read_groups_kernel<D, QSA_CODE_E4M3>);
+        case QSA_CODE_INT8: return launch(code_groups_kernel<D, QSA_CODE_INT8>, read_groups_kernel<D, QSA_CODE_INT8>);
+        case QSA_CODE_E2M1: return launch(code_groups_kernel<D, QSA_CODE_E2M1>, read_groups_kernel<D, QSA_CODE_E2M1>);
+        case QSA_CODE_INT4: return launch(code_groups_kernel<D, QSA_CODE_INT4>, read_groups_kernel<D, QSA_CODE_INT4>);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch(const CodeArgs &a, bool back, cudaStream_t s)
+{
+    if (a.batch == 0 || a.max_groups == 0) return cudaSuccess;
+    if (a.head_dim == 128) return launch_d<128>(a, back, s);
+    if (a.head_dim == 64) return launch_d<64>(a, back, s);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_code_groups(const CodeArgs &a, cudaStream_t s)
-{
-    if (a.batch == 0 || a.max_groups == 0) return cudaSuccess;
-    const int64_t blocks = (int64_t(a.max_groups) * a.kv_heads + kWarps - 1) / kWarps;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const dim3 grid(unsigned(blocks), unsigned(a.batch));
-    const bool i8 = a.format == QSA_CODE_INT8;
-    auto launch = [&](void (*kernel)(const CodeArgs)) { return launch_kernel(kernel, grid, dim3(kThreads), 0, s, true, a); };
-    if (a.head_dim == 128) return launch(i8 ? code_groups_kernel<128, true> : code_groups_kernel<128, false>);
-    if (a.head_dim == 64) return launch(i8 ? code_groups_kernel<64, true> : code_groups_kernel<64, false>);
-    return cudaErrorInvalidValue;
-}
+cudaError_t launch_code_groups(const CodeArgs &a, cudaStream_t s) { return launch(a, false, s); }
+cudaError_t launch_read_groups(const CodeArgs &a, cudaStream_t s) { return launch(a, true, s); }
 
 }  // namespace qsa

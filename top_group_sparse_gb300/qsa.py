@@ -1,4 +1,4 @@
-"""Thin ctypes binding of libqsa (``include/qsa.h``) -- argument marshalling only.
+"""Thin ctypes binding of libqsa (``include/qsa.h``, ``qsa_cache.h``, ``qsa_rows.h``) -- argument marshalling only.
 
 Every function carries the name of the C entry point it calls and does
 nothing but turn torch tensors (device memory) and plain Python values into
@@ -26,6 +26,9 @@ __all__ = [
     "QSA_DEVERR_WAIT_TIMEOUT",
     "QsaCodedCache", "QsaHistory", "qsa_code_groups", "qsa_coded_workspace_size", "qsa_attend_coded",
     "qsa_decode_coded", "qsa_evict_select", "qsa_evict_compact", "QSA_CODE_E4M3", "QSA_CODE_INT8",
+    "QSA_CODE_E2M1", "QSA_CODE_INT4", "code_bytes", "QsaProjection", "QsaRotation", "QsaNewTokens", "qsa_append_tokens",
+    "qsa_read_groups", "QSA_ROWS_F32", "QSA_ROWS_BF16", "QSA_ROWS_F16", "QSA_PAIR_HALVES", "QSA_PAIR_NEIGHBOURS",
+    "QSA_MAX_AXES", "QSA_ROWS_WORKSPACE_BYTES",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +43,12 @@ QSA_DEVERR_WAIT_TIMEOUT = 0x8
 QSA_DEVERR_NOT_SHARED = 0x10
 QSA_CODE_E4M3 = 0
 QSA_CODE_INT8 = 1
+QSA_CODE_E2M1 = 4
+QSA_CODE_INT4 = 5
+QSA_ROWS_F32, QSA_ROWS_BF16, QSA_ROWS_F16 = 0, 1, 2
+QSA_PAIR_HALVES, QSA_PAIR_NEIGHBOURS = 0, 1
+QSA_MAX_AXES = 4
+QSA_ROWS_WORKSPACE_BYTES = 256
 
 
 class QsaError(RuntimeError):
@@ -80,7 +89,7 @@ class QsaCodedCache(ctypes.Structure):
 
     @classmethod
     def of(cls, codes, scales, block_map, block_offset, fmt):
-        """From tensors: codes [num_blocks, n_kv, 8*d] (uint8), scales [num_blocks, n_kv, 2]."""
+        """From tensors: codes [num_blocks, n_kv, code_bytes(fmt, d)] (uint8), scales [num_blocks, n_kv, 2]."""
         return cls(_ptr(codes), _ptr(scales), int(codes.shape[0]), _ptr(block_map), _ptr(block_offset), int(fmt))
 
 
@@ -96,8 +105,67 @@ class QsaHistory(ctypes.Structure):
         return cls(**{k: _ptr(v) for k, v in members.items()})
 
 
+class QsaProjection(ctypes.Structure):
+    """qsa_projection (include/qsa_rows.h)."""
+    _fields_ = [("rows", ctypes.c_void_p), ("stride", ctypes.c_int64), ("norm", ctypes.c_void_p)]
+
+
+class QsaRotation(ctypes.Structure):
+    """qsa_rotation (include/qsa_rows.h)."""
+    _fields_ = [("freq", ctypes.c_void_p), ("dims", ctypes.c_int32), ("pairing", ctypes.c_int32)]
+
+
+class QsaNewTokens(ctypes.Structure):
+    """qsa_new_tokens (include/qsa_rows.h).  It holds pointers: the tensors it was made from have to live as
+    long as it is used."""
+    _fields_ = ([(n, QsaProjection) for n in ("q", "k", "v", "q_idx", "idx_key")] +
+                [("type", ctypes.c_int32), ("axes", ctypes.c_int32), ("positions", ctypes.c_void_p),
+                 ("turn", QsaRotation), ("turn_idx", QsaRotation), ("eps", ctypes.c_float)])
+
+    @classmethod
+    def of(cls, q=None, k=None, v=None, q_idx=None, idx_key=None, *, positions=None, freq=None, idx_freq=None,
+           pairing=QSA_PAIR_HALVES, idx_pairing=None, q_norm=None, k_norm=None, q_idx_norm=None, idx_key_norm=None,
+           eps=1e-6):
+        """From tensors: the projections, one row per query with its heads side by side ([B, heads * width] or
+        [B, heads, width], rows any stride apart), all of one type (float32, bfloat16, float16); positions
+        [axes, B] or [B] int32; freq, idx_freq [axes, dims / 2] or [dims / 2] f32; norms [width] f32."""
+        import torch
+        given = {"q": (q, q_norm), "k": (k, k_norm), "v": (v, None), "q_idx": (q_idx, q_idx_norm),
+                 "idx_key": (idx_key, idx_key_norm)}
+        types = {torch.float32: QSA_ROWS_F32, torch.bfloat16: QSA_ROWS_BF16, torch.float16: QSA_ROWS_F16}
+        dtypes = {x.dtype for x, _ in given.values() if x is not None}
+        if len(dtypes) != 1 or not dtypes <= set(types):
+            raise ValueError(f"the projections have one type of float32, bfloat16 and float16, not {dtypes or 'none'}")
+        made = {}
+        for name, (x, norm) in given.items():
+            if x is None:
+                if norm is not None:
+                    raise ValueError(f"{name}_norm without {name}")
+                continue
+            if not 2 <= x.dim() <= 3 or x.stride(-1) != 1 or (x.dim() == 3 and x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+                raise ValueError(f"{name}: one row per query, its heads side by side")
+            # (the stride of a single row says nothing)
+            width = x.shape[1] * (x.shape[2] if x.dim() == 3 else 1)
+            made[name] = QsaProjection(_ptr(x), int(x.stride(0)) if x.shape[0] > 1 else width, _f32(name + "_norm", norm))
+        axes = 1 if positions is None or positions.dim() == 1 else int(positions.shape[0])
+        if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
+            raise ValueError("positions: int32, contiguous")
+
+        def rotation(name, f, pair):
+            if f is None or f.numel() == 0:
+                return QsaRotation(None, 0, int(pair))
+            if (1 if f.dim() == 1 else f.shape[0]) != axes:
+                raise ValueError(f"{name} has a row for each of the {axes} axes of positions")
+            return QsaRotation(_f32(name, f), 2 * int(f.shape[-1]), int(pair))
+
+        return cls(type=types[dtypes.pop()], axes=axes, positions=_ptr(positions), eps=float(eps),
+                   turn=rotation("freq", freq, pairing),
+                   turn_idx=rotation("idx_freq", idx_freq, pairing if idx_pairing is None else idx_pairing), **made)
+
+
 _lib = None
 _P = ctypes.c_void_p
+_NP = ctypes.POINTER(QsaNewTokens)
 _CP = ctypes.POINTER(QsaCodedCache)
 _HP = ctypes.POINTER(QsaHistory)
 _DP = ctypes.POINTER(QsaDims)
@@ -181,6 +249,10 @@ def load(path: str | None = None):
     L.qsa_evict_select.restype = ctypes.c_int
     L.qsa_evict_compact.argtypes = [_DP, ctypes.c_int32, _P, _P, _HP, _HP, _P, ctypes.c_size_t, _P]
     L.qsa_evict_compact.restype = ctypes.c_int
+    L.qsa_append_tokens.argtypes = [_DP, _IP, _NP, _P, ctypes.c_size_t, _P]
+    L.qsa_append_tokens.restype = ctypes.c_int
+    L.qsa_read_groups.argtypes = [_DP, _IP, _CP, _P, _P, ctypes.c_int32, _P, ctypes.c_size_t, _P]
+    L.qsa_read_groups.restype = ctypes.c_int
     if path is None:
         _lib = L
     return L
@@ -203,6 +275,14 @@ def _ptr(x) -> int | None:
     if isinstance(x, int):
         return x
     return int(x.data_ptr())
+
+
+def _f32(name, x) -> int | None:
+    """Pointer of a contiguous float32 tensor (None: NULL)."""
+    import torch
+    if x is not None and (x.dtype != torch.float32 or not x.is_contiguous()):
+        raise ValueError(f"{name}: float32, contiguous")
+    return _ptr(x)
 
 
 def _stream(stream) -> int | None:
@@ -470,6 +550,30 @@ def qsa_evict_compact(dims, keep_groups, kept, n_kept, src, dst, ws, stream=None
         _stream(stream)))
 
 
+# ---- rows into the caches and back (include/qsa_rows.h) ----------------------
+
+def code_bytes(fmt: int, head_dim: int) -> int:
+    """Bytes of one (group, KV head)'s codes in a coded cache."""
+    return 9 * head_dim // 2 if fmt in (QSA_CODE_E2M1, QSA_CODE_INT4) else 8 * head_dim
+
+
+def qsa_append_tokens(dims, inputs, tokens, ws, stream=None) -> int:
+    """Normalises and rotates the new token (the last visible one) of every query and writes it where `inputs`
+    points: q, q_idx, its row of idx_keys, its slot of k_cache / v_cache."""
+    p, n = _ws(ws)
+    return _check("qsa_append_tokens", load().qsa_append_tokens(
+        ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(tokens), p, n, _stream(stream)))
+
+
+def qsa_read_groups(dims, inputs, cache, group_begin, group_end, max_groups, ws, stream=None) -> int:
+    """Writes groups [group_begin[b], group_end[b]) of every query from its blocks of the coded cache back to their
+    rows of k_cache / v_cache."""
+    p, n = _ws(ws)
+    return _check("qsa_read_groups", load().qsa_read_groups(
+        ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(cache), _ptr(group_begin), _ptr(group_end),
+        int(max_groups), p, n, _stream(stream)))
+
+
 # ---- device-resident batch (plumbing: torch owns the memory) ----------------
 
 def _packed(arrays, device):
@@ -710,7 +814,12 @@ class DeviceBatch:
         return qsa_decode_pooled(self.dims, self.inputs, self.pooled, self.pool_offset, self.ids,
                                  self.n_ids, self.out, self.ws, stream)
 
-    # ---- a K/V cache in 8 bits ------------------------------------------------
+    # ---- new tokens -------------------------------------------------------------
+    def append(self, tokens, stream=None):
+        """Writes the batch's new tokens (a QsaNewTokens) into q, q_idx, idx_keys and the K/V cache."""
+        return qsa_append_tokens(self.dims, self.inputs, tokens, self.ws, stream)
+
+    # ---- a K/V cache in 8 or 4 bits ---------------------------------------------
     def make_coded_cache(self, fmt=QSA_CODE_E4M3):
         """Allocates the coded cache: one block per complete group of each distinct
         history (in order), its accumulated weights (one per group and one for an
@@ -733,7 +842,7 @@ class DeviceBatch:
 
         self.block_offset, self.weight_offset = put(block), put(weight)
         self.block_map = torch.arange(max(blocks, 1), dtype=torch.int32, device=dev)
-        self.codes = torch.zeros((max(blocks, 1), w.kv_heads, 8 * w.head_dim), dtype=torch.uint8, device=dev)
+        self.codes = torch.zeros((max(blocks, 1), w.kv_heads, code_bytes(fmt, w.head_dim)), dtype=torch.uint8, device=dev)
         self.scales = torch.zeros((max(blocks, 1), w.kv_heads, 2), dtype=torch.float32, device=dev)
         self.weights = torch.zeros(max(weights, 1), dtype=torch.float32, device=dev)
         self.coded = QsaCodedCache.of(self.codes, self.scales, self.block_map, self.block_offset, fmt)
@@ -754,6 +863,17 @@ class DeviceBatch:
             args = torch.from_numpy(np.stack([gb, ge])).to(self.q.device)
             return qsa_code_groups(self.dims, self.inputs, self.coded, args[0], args[1],
                                    max(int((ge - gb).max(initial=0)), 0), self.coded_ws, handle)
+
+    def read_back(self, stream=None):
+        """Writes every complete group of every history from its codes back to its rows of k_cache / v_cache."""
+        import torch
+        ge = np.where(self._code_owner, self.visible.cpu().numpy() // 4, 0).astype(np.int32)
+        handle = _stream(stream)
+        on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        with torch.cuda.stream(on):
+            args = torch.from_numpy(np.stack([np.zeros_like(ge), ge])).to(self.q.device)
+            return qsa_read_groups(self.dims, self.inputs, self.coded, args[0], args[1], int(ge.max(initial=0)),
+                                   self.coded_ws, handle)
 
     def code_all(self, stream=None):
         """Codes every complete group of every history (once per history)."""
