@@ -29,7 +29,6 @@ bool add(AppendFamily &f, int i, const qsa_projection &p, int heads, int width, 
     f.norm[i] = p.norm;
     f.out[i] = static_cast<float *>(const_cast<void *>(out));
     f.heads[i] = heads;
-    if (p.norm != nullptr) f.any_norm = 1;
     return true;
 }
 
@@ -78,8 +77,6 @@ qsa_status qsa_append_tokens(const qsa_dims *dims, const qsa_inputs *in, const q
     const qsa_status st = check_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
     if (dims->batch == 0) return QSA_OK;
-    a.family[0].out_heads = dims->kv_heads;
-    a.family[1].out_heads = 1;
     a.positions = t.positions;
     a.visible = in->visible;
     a.slot_map = in->slot_map;

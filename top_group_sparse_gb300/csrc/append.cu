@@ -8,13 +8,13 @@
 // integer product with 1/(2 pi), and pos * F modulo 2^64 is the angle modulo a full turn
 // for every position.  Sine and cosine are then of a binary32 number of half turns.
 //
-// Layout.  A lane holds four neighbouring dims, so a head is a quarter of its width in
-// lanes (a warp takes 1, 2 or 4 heads at once) and every access is a 16-byte (or, of
-// 16-bit types, 8-byte) piece of a row.  The partner of a dim is in the same lane
-// (neighbours) or in another at a fixed distance (halves: dims is a multiple of 8), so a
-// rotation is z = y * cos + partner * (+-sin) everywhere.  A warp takes consecutive heads
-// of one token and computes its sines once for all of them: all the heads of a token when
-// there are enough tokens to fill the GPU, else as few as one step.
+// Layout.  A lane holds eight neighbouring dims (two quads), so a head is an eighth of its
+// width in lanes, a warp takes 2, 4 or 8 heads of one projection (a step), and 16-bit rows
+// come in 16-byte pieces and leave in 32-byte ones.  A warp keeps its step -- pointers, norm
+// weights -- and walks over tokens, a few at a time whose loads are out together; the CTA's
+// warps are a token's steps and make its table of cos and signed sin per dim together.  The
+// partner of a dim is in the same lane (neighbours) or a fixed number of quads away (halves:
+// dims is a multiple of 8), so a rotation is z = y * cos + partner * (+-sin) for both.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,16 +23,19 @@
 namespace qsa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 6;
-constexpr int kWarpsWanted = 64;      // tasks per SM below which a token's heads are spread over more warps
-constexpr int kMaxPairs = 64;
+constexpr int kMaxWarps = 16;
+constexpr int kMaxWidth = 128;
+constexpr int kTokens = 4;             // of a CTA at a time, at most (32-bit rows: half as many)
+constexpr int kRegisters = 48;
 
 struct Table {
-    uint64_t turns[2][QSA_MAX_AXES][kMaxPairs];  // by family: heads of d, heads of d_I
-    float bad[2][kMaxPairs];                     // NaN for a pair with a frequency out of range, else 0
+    uint64_t turns[2][QSA_MAX_AXES][kMaxWidth / 2];  // by family: heads of d, heads of d_I
+    float bad[2][kMaxWidth / 2];                     // NaN for a pair with a frequency out of range, else 0
+    // [two batches of tokens]: of dim 8l + 4h + i at [h * width/2 + 4l + i], free of bank conflicts
+    float cosine[2][kTokens][2][kMaxWidth], sine[2][kTokens][2][kMaxWidth];
 };
+
+__device__ __forceinline__ int place_of(int dim, int width) { return (dim / 4 % 2) * (width / 2) + dim / 8 * 4 + dim % 4; }
 
 // f / (2 pi) as a fraction of a turn (modulo 1, in units of 2^-64) for |f| < 2^16.
 __device__ __forceinline__ uint64_t turns_of(float f)
@@ -49,194 +52,319 @@ __device__ __forceinline__ uint64_t turns_of(float f)
     return bits >> 31 ? 0 - t : t;
 }
 
-template <typename T>
-struct Raw { using type = uint2; };
-template <>
-struct Raw<float> { using type = float4; };
-
-template <typename T>
-__device__ __forceinline__ float4 widen(typename Raw<T>::type r)
+// Two binary32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    if constexpr (sizeof(T) == 4) {
-        return r;
-    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                           __uint_as_float(r.y & 0xffff0000u));
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// Eight elements of a row, a lane's own, on their way through shared memory.
+template <typename T>
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void fetch(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(T) / 2); ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(v + i)), "l"(p + i * (16 / sizeof(T))) : "memory");
+    }
+    __device__ __forceinline__ void widen(float2 (&x)[4]) const
+    {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[2 * i] = make_float2(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                x[2 * i + 1] = make_float2(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
+            }
+        } else {
+            const uint4 r = v[0];
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same<T, __nv_bfloat16>::value)
+                    x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+                else
+                    x[i] = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            }
+        }
+    }
+};
+
+// 32 bytes at once where they are so aligned: in 16-byte pieces a warp's store would touch every
+// 32-byte sector twice.
+__device__ __forceinline__ void store(float *p, const float2 (&x)[4], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(x[0].x), "f"(x[0].y), "f"(x[1].x),
+                     "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y)
+                     : "memory");
     } else {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&r.x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&r.y));
-        return make_float4(a.x, a.y, b.x, b.y);
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
     }
 }
 
-// Heads [step * (128/W), ..) of one family of token b, `steps` steps of them, by a warp.
-template <typename T, int W, int kFamily>
-__device__ __forceinline__ void append_heads(const AppendArgs &a, const Table &table, int b, int step, int steps)
+// What a thread makes of a token's table: pair p of each u-th of a batch's tokens.
+struct Angle {
+    int p, p_step, u, u_step;
+};
+struct Position {
+    int at[QSA_MAX_AXES];
+};
+__device__ __forceinline__ Position position_of(const AppendArgs &a, int b)
 {
-    constexpr int kLanes = W / 4, kRows = 32 / kLanes;
-    const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+    Position r;
+#pragma unroll
+    for (int x = 0; x < QSA_MAX_AXES; ++x) r.at[x] = x < a.axes && b < a.batch ? __ldg(a.positions + int64_t(x) * a.batch + b) : 0;
+    return r;
+}
+
+// `first`: the position of the first of the thread's tokens.
+__device__ __forceinline__ void make_angles(const AppendArgs &a, Table &table, const Angle &mine, int pairs0, int pairs, int d, int di,
+                                            int buffer, int b0, int n, const Position &first)
+{
+    for (int p = mine.p; p < pairs; p += mine.p_step) {
+        const int fam = p < pairs0 ? 0 : 1, j = fam == 0 ? p : p - pairs0, side = fam == 0 ? pairs0 : pairs - pairs0;
+        const int width = fam == 0 ? d : di;
+        const bool neighbours = fam == 0 ? a.family[0].neighbours : a.family[1].neighbours;
+        const int one = place_of(neighbours ? 2 * j : j, width), two = place_of(neighbours ? 2 * j + 1 : j + side, width);
+        const float bad = table.bad[fam][j];
+        for (int u = mine.u; u < n; u += mine.u_step) {
+            const Position pos = u == mine.u ? first : position_of(a, b0 + u);
+            uint32_t phase = 0;  // the upper half of the products' sum modulo 2^64, but for the lower halves' carries
+#pragma unroll
+            for (int x = 0; x < QSA_MAX_AXES; ++x)
+                if (x < a.axes) {
+                    const uint64_t t = table.turns[fam][x][j];
+                    const uint32_t at = uint32_t(pos.at[x]);
+                    phase += __umulhi(at, uint32_t(t)) + at * uint32_t(t >> 32) - (pos.at[x] < 0 ? uint32_t(t) : 0u);
+                }
+            float s, c;
+            sincospif(float(int32_t(phase)) * 0x1p-31f, &s, &c);  // half turns
+            float *const cosine = table.cosine[buffer][u][fam], *const sine = table.sine[buffer][u][fam];
+            cosine[one] = cosine[two] = c + bad;
+            sine[one] = -s + bad;
+            sine[two] = s + bad;
+        }
+    }
+}
+
+// Step `step` of one family for all the CTA's tokens, a.tokens at a time: batches blockIdx.x,
+// blockIdx.x + gridDim.x, ..  Control is the same for the whole warp throughout.
+template <typename T, int W, int kFamily>
+__device__ __forceinline__ void append_step(const AppendArgs &a, Table &table, Raw<T> *ring, const Angle &mine, int pairs0, int pairs, int d, int di,
+                                            int step)
+{
+    constexpr int kMost = sizeof(T) == 4 ? kTokens / 2 : kTokens;
+    constexpr int kLanes = W / 8, kRows = 32 / kLanes;
+    const int lane = threadIdx.x & 31, l = lane % kLanes;
     const AppendFamily &f = a.family[kFamily];
-    using R = typename Raw<T>::type;
-
-    // the row's head, by the order q, k, v (q_idx, idx_key)
-    auto part_of = [&](int head, int &at) {
-        int k = 0;
-        at = head;
+    const bool any = step < f.steps;
+    int kind = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (at >= f.heads[i] && k == i) {
-                at -= f.heads[i];
-                k = i + 1;
-            }
-        return k;
-    };
-    auto load = [&](int s) {
-        const int head = (step + s) * kRows + sub;
-        R r{};
-        if (s < steps && head < f.all_heads) {
-            int at;
-            const int k = part_of(head, at);
-            r = __ldg(reinterpret_cast<const R *>(static_cast<const T *>(f.rows[k]) + b * f.stride[k] + at * W) + l);
-        }
-        return r;
-    };
-    R next = load(0);
-
-    // where the token goes
-    const int vis = __ldg(a.visible + b);
-    const bool in_range = vis >= 0 && vis <= a.max_visible;
-    if (vis == 0) return;
-    int64_t row = -1;  // of the caches, or of idx_keys
-    if (!in_range) {
-        if (step == 0 && lane == 0) set_error(a.err, QSA_DEVERR_VISIBLE_RANGE);
-    } else if constexpr (kFamily == 0) {
-        if (f.heads[1] + f.heads[2] > 0) {
-            const int slot = __ldg(a.slot_map + __ldg(a.slot_offset + b) + vis - 1);
-            if (slot >= 0 && slot < a.num_slots) row = slot;
-            else if (step == 0 && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
-        }
-    } else {
-        if (f.heads[1] > 0) row = __ldg(a.key_offset + b) + vis - 1;
+    for (int k = 0; k < 2; ++k)
+        if (kind == k && step >= f.kind_steps[k]) step -= f.kind_steps[k], kind = k + 1;
+    const int head = step * kRows + lane / kLanes, heads = any ? f.heads[kind] : 0;
+    const bool there = head < heads;
+    const T *src = static_cast<const T *>(f.rows[kind]) + int64_t(head) * W + 8 * l;
+    const int64_t stride = f.stride[kind];
+    float *const dst = f.out[kind] + int64_t(head) * W + 8 * l;
+    const bool normed = any && f.norm[kind] != nullptr;
+    float2 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = normed ? __ldg(reinterpret_cast<const float2 *>(f.norm[kind] + 8 * l) + i) : make_float2(0.f, 0.f);
+    const int apart = any && !(kFamily == 0 && kind == 2) ? f.dims / 8 : 0;  // quads
+    int partner[2];                  // lanes of the partners of this lane's quads (halves)
+    bool turned[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int quad = 2 * l + h;
+        turned[h] = quad < 2 * apart;
+        partner[h] = turned[h] ? lane - l + (quad < apart ? quad + apart : quad - apart) / 2 : lane;
     }
 
-    // this lane's four dims: cos, and the factor of their partners
-    const int half = f.dims / 2;
-    const bool turned = 4 * l < f.dims;
-    int partner = lane;
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-    if (f.dims > 0) {
-        const bool second = 4 * l >= half;
-        if (!f.neighbours && turned) partner = second ? lane - half / 4 : lane + half / 4;
-        const int j0 = !turned ? 0 : f.neighbours ? 2 * l : second ? 4 * l - half : 4 * l;
-        const int n = f.neighbours ? 2 : 4;
+    // a batch's loads, this lane's pieces of its tokens at ring[u * threads], go out a batch ahead
+    ring += threadIdx.x;
+    const int threads = blockDim.x;
+    auto fetch = [&](int first, int buffer) {
+        const int n = there ? min(a.tokens, a.batch - first) : 0;
+        const T *p = src + first * stride;
+        Raw<T> *to = ring + buffer * (kMost * threads);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < kMost; ++u, p += stride, to += threads)
+            if (u < n) to->fetch(p);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // the elements of `out` before the row that token first + u goes to: lane u looks it up.  -1: none,
+    // and of a query that is out of range -2 - that, for zeros
+    auto look_up = [&](int first) {
+        int64_t at = -1;
+        if (lane < min(a.tokens, a.batch - first) && any) {
+            const int b = first + lane, vis = __ldg(a.visible + b);
+            if (vis < 0 || vis > a.max_visible) {
+                set_error(a.err, QSA_DEVERR_VISIBLE_RANGE);
+                at = kind == 0 ? -2 - int64_t(b) * (heads * W) : -1;
+            } else if (vis > 0) {
+                if (kind == 0) {
+                    at = b;
+                } else if (kFamily == 1) {
+                    at = __ldg(a.key_offset + b) + vis - 1;
+                } else {
+                    const int slot = __ldg(a.slot_map + __ldg(a.slot_offset + b) + vis - 1);
+                    if (slot >= 0 && slot < a.num_slots) at = slot;
+                    else set_error(a.err, QSA_DEVERR_SLOT_RANGE);
+                }
+                if (at >= 0) at *= heads * W;
+            }
+        }
+        return at;
+    };
+    // Before a batch's arithmetic everything is asked for that the next one needs; its table is made
+    // behind it, into the other half, which every warp is done with since the last barrier.
+    const int stepped = int(gridDim.x) * a.tokens;
+    int first = int(blockIdx.x) * a.tokens, buffer = 0;
+    fetch(first, 0);
+    int64_t to = look_up(first);
+    make_angles(a, table, mine, pairs0, pairs, d, di, 0, first, min(a.tokens, a.batch - first), position_of(a, first + mine.u));
+    while (first < a.batch) {
+        const int n = min(a.tokens, a.batch - first), next = first + stepped;
+        fetch(next, buffer ^ 1);
+        const int64_t next_to = look_up(next);
+        const Position next_position = position_of(a, next + mine.u);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
             if (u >= n) break;
-            uint64_t phase = 0;
-            for (int x = 0; x < a.axes; ++x)
-                phase += uint64_t(int64_t(__ldg(a.positions + int64_t(x) * a.batch + b))) * table.turns[kFamily][x][j0 + u];
-            float s0, c0;
-            sincospif(float(int32_t(phase >> 32)) * 0x1p-31f, &s0, &c0);  // half turns
-            c[u] = c0 + table.bad[kFamily][j0 + u];
-            sn[u] = s0 + table.bad[kFamily][j0 + u];
-        }
-        if (f.neighbours) {
-            c[3] = c[2] = c[1];
-            sn[3] = sn[1];
-            sn[2] = -sn[1];
-            c[1] = c[0];
-            sn[1] = sn[0];
-            sn[0] = -sn[0];
-        } else if (!second) {
+            float2 x[4];
+            ring[(buffer * kMost + u) * threads].widen(x);
+            if (normed) {
+                float2 sq = mul2(x[0], x[0]);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sn[u] = -sn[u];
+                for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
+                float ss = sq.x + sq.y;
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float r = rsqrtf(fmaf(ss, 1.0f / W, a.eps));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = mul2(mul2(x[i], make_float2(r, r)), w[i]);
+            }
+            if (apart > 0) {
+                float2 y[4];
+                if (f.neighbours) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = make_float2(x[i].y, x[i].x);
+                } else {
+                    const bool other = apart % 2 != 0;  // an odd number of quads away: the other quad of that lane
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        y[i].x = __shfl_sync(0xffffffffu, other ? x[i ^ 2].x : x[i].x, partner[i / 2]);
+                        y[i].y = __shfl_sync(0xffffffffu, other ? x[i ^ 2].y : x[i].y, partner[i / 2]);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 c = *reinterpret_cast<const float4 *>(&table.cosine[buffer][u][kFamily][h * (W / 2) + 4 * l]);
+                    const float4 s = *reinterpret_cast<const float4 *>(&table.sine[buffer][u][kFamily][h * (W / 2) + 4 * l]);
+                    const float2 z0 = fma2(x[2 * h], make_float2(c.x, c.y), mul2(y[2 * h], make_float2(s.x, s.y)));
+                    const float2 z1 = fma2(x[2 * h + 1], make_float2(c.z, c.w), mul2(y[2 * h + 1], make_float2(s.z, s.w)));
+                    if (turned[h]) x[2 * h] = z0, x[2 * h + 1] = z1;
+                }
+            }
+            int64_t at = __shfl_sync(0xffffffffu, to, u);
+            if (at < -1) {
+                at = -2 - at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = make_float2(0.0f, 0.0f);
+            }
+            if (there && at >= 0) store(dst + at, x, f.wide);
         }
+        first = next;
+        to = next_to;
+        buffer ^= 1;
+        make_angles(a, table, mine, pairs0, pairs, d, di, buffer, first, min(a.tokens, a.batch - first), next_position);
     }
+}
 
-    for (int s = 0; s < steps; ++s) {
-        const R raw = next;
-        next = load(s + 1);
-        const int head = (step + s) * kRows + sub;
-        int at;
-        const int k = part_of(head, at);
-        const bool some = head < f.all_heads;
-        float4 x = widen<T>(raw);
-        if (f.any_norm) {
-            float ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, x.w * x.w)));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (some && f.norm[k] != nullptr) {
-                const float4 w = __ldg(reinterpret_cast<const float4 *>(f.norm[k]) + l);
-                const float r = __frsqrt_rn(fmaf(ss, 1.0f / W, a.eps));
-                x = make_float4(x.x * r * w.x, x.y * r * w.y, x.z * r * w.z, x.w * r * w.w);
-            }
+// A CTA's warps are the steps blockIdx.y * warps .. of a token.
+template <typename T, int D, int DI>
+__global__ void __maxnreg__(kRegisters) append_kernel(const __grid_constant__ AppendArgs a)
+{
+    extern __shared__ __align__(16) unsigned char smem_raw[];  // the table; two batches of raw pieces
+    Table &table = *reinterpret_cast<Table *>(smem_raw);
+    Raw<T> *const ring = reinterpret_cast<Raw<T> *>(smem_raw + sizeof(Table));
+    const int tid = threadIdx.x, threads = blockDim.x;
+    wait_for_predecessor();
+    const int pairs0 = a.family[0].dims / 2, pairs = pairs0 + a.family[1].dims / 2;
+    for (int i = tid; i < pairs; i += threads) {
+        const int fam = i < pairs0 ? 0 : 1, j = fam == 0 ? i : i - pairs0, n = fam == 0 ? pairs0 : pairs - pairs0;
+        float bad = 0.0f;
+        for (int x = 0; x < a.axes; ++x) {
+            const float freq = __ldg((fam == 0 ? a.family[0].freq : a.family[1].freq) + x * n + j);
+            const bool ok = fabsf(freq) < 65536.0f;
+            table.turns[fam][x][j] = ok ? turns_of(freq) : 0;
+            if (!ok) bad = __int_as_float(0x7fffffff);
         }
-        if (f.dims > 0) {
-            float4 p;
-            if (f.neighbours) {
-                p = make_float4(x.y, x.x, x.w, x.z);
-            } else {
-                p.x = __shfl_sync(0xffffffffu, x.x, partner);
-                p.y = __shfl_sync(0xffffffffu, x.y, partner);
-                p.z = __shfl_sync(0xffffffffu, x.z, partner);
-                p.w = __shfl_sync(0xffffffffu, x.w, partner);
-            }
-            if (turned && !(kFamily == 0 && k == 2))
-                x = make_float4(fmaf(x.x, c[0], p.x * sn[0]), fmaf(x.y, c[1], p.y * sn[1]), fmaf(x.z, c[2], p.z * sn[2]),
-                                fmaf(x.w, c[3], p.w * sn[3]));
-        }
-        if (!some) continue;
-        if (k == 0) {  // the batch's own rows; zeros for a query that is out of range
-            if (!in_range) x = make_float4(0.f, 0.f, 0.f, 0.f);
-            *(reinterpret_cast<float4 *>(f.out[0] + (int64_t(b) * f.heads[0] + at) * W) + l) = x;
-        } else if (row >= 0) {
-            *(reinterpret_cast<float4 *>(f.out[k] + (row * f.out_heads + at) * W) + l) = x;
-        }
+        table.bad[fam][j] = bad;
     }
+    // fewer threads than pairs: a thread has several pairs of every token; else one pair of some tokens
+    Angle mine = {tid, threads, 0, 1};
+    if (pairs > 0 && threads >= pairs) {
+        mine = {tid % pairs, pairs, tid / pairs, threads / pairs};
+        if (mine.u >= mine.u_step) mine.u = kTokens;
+    }
+    __syncthreads();
+    const int step = int(blockIdx.y) * (threads / 32) + __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (step < a.family[0].steps) append_step<T, D, 0>(a, table, ring, mine, pairs0, pairs, D, DI, step);
+    else append_step<T, DI, 1>(a, table, ring, mine, pairs0, pairs, D, DI, step - a.family[0].steps);
 }
 
 template <typename T, int D, int DI>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) append_kernel(const __grid_constant__ AppendArgs a)
+cudaError_t launch_t(AppendArgs a, int num_sms, cudaStream_t s)
 {
-    __shared__ Table table;
-    const int tid = threadIdx.x, warp = tid >> 5;
-    wait_for_predecessor();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int pairs = a.family[i].dims / 2;
-        for (int j = tid; j < pairs; j += kThreads) {
-            float bad = 0.0f;
-            for (int x = 0; x < a.axes; ++x) {
-                const float f = __ldg(a.family[i].freq + x * pairs + j);
-                const bool ok = fabsf(f) < 65536.0f;
-                table.turns[i][x][j] = ok ? turns_of(f) : 0;
-                if (!ok) bad = __int_as_float(0x7fffffff);
-            }
-            table.bad[i][j] = bad;
-        }
+    constexpr int kMost = sizeof(T) == 4 ? kTokens / 2 : kTokens;
+    constexpr size_t kRing = size_t(2) * kMost * 32 * sizeof(Raw<T>);  // of a warp
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_done[dev]) {
+        e = cudaFuncSetAttribute(append_kernel<T, D, DI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 int(sizeof(Table) + kMaxWarps * kRing));
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = true;
     }
-    __syncthreads();
-    const int64_t tasks = int64_t(a.batch) * a.tasks;
-    for (int64_t t = int64_t(blockIdx.x) * kWarps + warp; t < tasks; t += int64_t(gridDim.x) * kWarps) {
-        const int b = int(t / a.tasks), k = int(t - int64_t(b) * a.tasks);
-        if (k < a.family[0].tasks) {
-            append_heads<T, D, 0>(a, table, b, k * a.steps, min(a.steps, a.family[0].steps - k * a.steps));
-        } else {
-            const int i = k - a.family[0].tasks;
-            append_heads<T, DI, 1>(a, table, b, i * a.steps, min(a.steps, a.family[1].steps - i * a.steps));
-        }
-    }
+    const int steps = a.family[0].steps + a.family[1].steps, cuts = (steps + kMaxWarps - 1) / kMaxWarps;
+    const int warps = (steps + cuts - 1) / cuts;
+    const size_t smem = sizeof(Table) + warps * kRing;
+    // as many CTAs as are resident; fewer tokens at a time where that leaves SMs without any
+    const int by_registers = 65536 / (kRegisters * 32 * warps), by_smem = int(228 * 1024 / (smem + 1024));
+    const int64_t resident = int64_t(num_sms) * (by_registers < by_smem ? by_registers : by_smem) / cuts;
+    const int64_t most = resident > 0 ? resident : 1, share = a.batch / most;
+    a.tokens = int(share < 1 ? 1 : share > kMost ? kMost : share);
+    const int64_t batches = (int64_t(a.batch) + a.tokens - 1) / a.tokens;
+    return launch_kernel(append_kernel<T, D, DI>, dim3(unsigned(batches < most ? batches : most), unsigned(cuts)),
+                         dim3(32 * warps), smem, s, true, a);
 }
 
 template <typename T>
-cudaError_t launch_t(const AppendArgs &a, int d, int idx, int num_sms, cudaStream_t s)
+cudaError_t launch_type(const AppendArgs &a, int d, int idx, int num_sms, cudaStream_t s)
 {
-    const int64_t ctas = (int64_t(a.batch) * a.tasks + kWarps - 1) / kWarps, most = int64_t(num_sms) * kCtasPerSm;
-    auto launch = [&](void (*kernel)(const AppendArgs)) {
-        return launch_kernel(kernel, dim3(unsigned(ctas < most ? ctas : most)), dim3(kThreads), 0, s, true, a);
-    };
-    if (d == 128) return launch(idx == 64 ? append_kernel<T, 128, 64> : append_kernel<T, 128, 32>);
-    return launch(idx == 64 ? append_kernel<T, 64, 64> : append_kernel<T, 64, 32>);
+    if (d == 128) return idx == 64 ? launch_t<T, 128, 64>(a, num_sms, s) : launch_t<T, 128, 32>(a, num_sms, s);
+    return idx == 64 ? launch_t<T, 64, 64>(a, num_sms, s) : launch_t<T, 64, 32>(a, num_sms, s);
 }
 
 }  // namespace
@@ -244,23 +372,18 @@ cudaError_t launch_t(const AppendArgs &a, int d, int idx, int num_sms, cudaStrea
 cudaError_t launch_append(AppendArgs a, int type, int d, int idx, int num_sms, cudaStream_t s)
 {
     if (a.batch == 0) return cudaSuccess;
-    auto cut = [&](int steps) {
-        a.steps = steps;
-        a.tasks = 0;
-        for (AppendFamily &f : a.family) a.tasks += f.tasks = (f.steps + steps - 1) / steps;
-    };
-    int most = 0;
     for (int i = 0; i < 2; ++i) {
         AppendFamily &f = a.family[i];
-        const int rows = 128 / (i == 0 ? d : idx);
-        f.all_heads = f.heads[0] + f.heads[1] + f.heads[2];
-        f.steps = (f.all_heads + rows - 1) / rows;
-        most = f.steps > most ? f.steps : most;
+        const int rows = 256 / (i == 0 ? d : idx);
+        f.steps = 0;
+        f.wide = 1;
+        for (const float *out : f.out) f.wide &= reinterpret_cast<uintptr_t>(out) % 32 == 0;
+        for (int k = 0; k < 3; ++k) f.steps += f.kind_steps[k] = (f.heads[k] + rows - 1) / rows;
     }
-    for (cut(most); a.steps > 1 && int64_t(a.batch) * a.tasks < int64_t(num_sms) * kWarpsWanted;) cut((a.steps + 1) / 2);
-    if (type == QSA_ROWS_F32) return launch_t<float>(a, d, idx, num_sms, s);
-    if (type == QSA_ROWS_BF16) return launch_t<__nv_bfloat16>(a, d, idx, num_sms, s);
-    return launch_t<__half>(a, d, idx, num_sms, s);
+    if ((int64_t(a.family[0].steps) + a.family[1].steps + kMaxWarps - 1) / kMaxWarps > 65535) return cudaErrorInvalidValue;
+    if (type == QSA_ROWS_F32) return launch_type<float>(a, d, idx, num_sms, s);
+    if (type == QSA_ROWS_BF16) return launch_type<__nv_bfloat16>(a, d, idx, num_sms, s);
+    return launch_type<__half>(a, d, idx, num_sms, s);
 }
 
 }  // namespace qsa

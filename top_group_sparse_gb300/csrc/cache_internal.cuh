@@ -104,10 +104,10 @@ struct AppendFamily {
     const float *norm[3];
     float *out[3];          // [0]: a row per query; the others: by slot, or by logical row
     int32_t heads[3];       // 0: not given
-    int32_t out_heads;      // heads of a row of out[1], out[2]
-    int32_t any_norm, dims, neighbours;
+    int32_t dims, neighbours;
     const float *freq;
-    int32_t all_heads, steps, tasks;  // the launcher's: a step is 128/width heads, a task some steps
+    int32_t kind_steps[3], steps;  // the launcher's: a step is 256/width heads of a projection
+    int32_t wide;           // every out is 32-byte aligned
 };
 struct AppendArgs {
     AppendFamily family[2];
@@ -116,7 +116,7 @@ struct AppendArgs {
     int64_t num_slots;
     float eps;
     int32_t axes, batch, max_visible;
-    int32_t steps, tasks;   // the launcher's: steps of a task, tasks of a token
+    int32_t tokens;         // the launcher's: of a CTA at a time
     uint32_t *err;
 };
 cudaError_t launch_append(AppendArgs a, int type, int head_dim, int idx_dim, int num_sms, cudaStream_t s);
