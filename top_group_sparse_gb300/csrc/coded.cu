@@ -18,9 +18,7 @@
 // t = e4m3(a / (c s)) and code = rn(x / (t s)) by the same quotients, t s being normal and
 // above 2^-90 where s is above 2^-80.  A word of K is two tiles of a token, so lanes exchange
 // their halves of it with their neighbours; a tile of V is 8 bytes of one lane.
-#include <cuda_fp16.h>
-
-#include "cache_internal.cuh"
+#include "codes4.cuh"
 
 namespace qsa {
 namespace {
@@ -112,12 +110,46 @@ __device__ __forceinline__ void code_rows(const float4 (&r)[4], int l, bool is_k
     }
 }
 
-// Two codes of 4 bits, |x| and |y| at most the format's largest (e2m1: more saturates), as
-// the low and the high half of a byte (e2m1), or x's code + 8 in the low four bits (int4).
-__device__ __forceinline__ uint32_t nibbles_int4(float x)
+// Two binary32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ float2 mul2(float2 a, float b)
 {
-    return __float_as_uint(__fadd_rn(x, 12582912.0f + 8.0f)) & 15u;  // as in code4; 8 is even
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b));
+    return r;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c)
+{
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// quotient() of two values, without the sign of a zero; minus_s: -s.
+__device__ __forceinline__ float2 quotient2(float2 x, float minus_s, float r)
+{
+    float2 q = mul2(x, r);
+    q = fma2(fma2(q, minus_s, x), r, q);
+    return fma2(fma2(q, minus_s, x), r, q);
+}
+
+// Four codes + 8 of 4-bit integers, each in four bits, in the low half of a word (the rest is
+// of no account): a sum with 1.5 * 2^23 + 8 rounds to the nearest integer, even on ties as 8 is,
+// and holds it, + 8, in the low bits of a number whose others are 0 below bit 22.
+__device__ __forceinline__ uint32_t four_int4(float a, float b, float c, float d)
+{
+    constexpr float kMagic = 12582912.0f + 8.0f;
+    uint32_t r = __float_as_uint(__fadd_rn(d, kMagic));
+    r = r * 16u + __float_as_uint(__fadd_rn(c, kMagic));
+    r = r * 16u + __float_as_uint(__fadd_rn(b, kMagic));
+    return r * 16u + __float_as_uint(__fadd_rn(a, kMagic));
+}
+
+// Pairs of values as e2m1 codes, the first in the low and the second in the high half of a byte;
+// what is larger than the largest code becomes that.
 __device__ __forceinline__ uint32_t bytes_e2m1(float2 a, float2 b, float2 c, float2 d)
 {
     uint32_t r;
@@ -158,9 +190,9 @@ __device__ __forceinline__ void code_rows4(const float4 (&r)[4], int l, bool is_
     const bool finite = bits < 0x7f800000u;
     float s = __fmul_rn(__uint_as_float(bits), kInt4 ? 1.0f / 3136.0f : 1.0f / 2688.0f);
     if (s < 1.17549435e-38f) s = 0.0f;
-    float y[4][4];  // [token][dim]
+    float2 y[4][2];  // [token][two dims]
 #pragma unroll
-    for (int u = 0; u < 4; ++u) y[u][0] = r[u].x, y[u][1] = r[u].y, y[u][2] = r[u].z, y[u][3] = r[u].w;
+    for (int u = 0; u < 4; ++u) y[u][0] = make_float2(r[u].x, r[u].y), y[u][1] = make_float2(r[u].z, r[u].w);
     uint32_t tile = 0;
     if (finite && s > 0.0f) {
         const float unit = __fmul_rn(kTop, s);
@@ -172,33 +204,40 @@ __device__ __forceinline__ void code_rows4(const float4 (&r)[4], int l, bool is_
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[u][j] = quotient<kInt4>(y[u][j], ts, inv);
+                for (int j = 0; j < 2; ++j) {
+                    const float2 x = y[u][j];
+                    y[u][j] = quotient2(x, -ts, inv);
+                    if constexpr (!kInt4) y[u][j] = make_float2(copysignf(y[u][j].x, x.x), copysignf(y[u][j].y, x.y));
+                }
         } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) y[u][j] = __fdiv_rn(y[u][j], ts);
+                for (int j = 0; j < 2; ++j) y[u][j] = make_float2(__fdiv_rn(y[u][j].x, ts), __fdiv_rn(y[u][j].y, ts));
         }
     }
+    // A normal e4m3 number is at most 1/17 below what was rounded to it, so the quotients stay below
+    // 7.44, or the e2m1 codes saturate; a subnormal one may be a third below, and 0 has no quotient.
+    if (tile < 8) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[u][j] = tile != 0 ? fminf(fmaxf(y[u][j], -kTop), kTop) : 0.0f;
+            for (int j = 0; j < 2; ++j)
+                y[u][j] = tile == 0 ? make_float2(0.0f, 0.0f)
+                                    : make_float2(fminf(fmaxf(y[u][j].x, -kTop), kTop), fminf(fmaxf(y[u][j].y, -kTop), kTop));
+    }
     if (l == 0) *scale_dst = finite ? s : __int_as_float(0x7fffffff);
     if (is_k) {
         const int j = l / 16, c = l % 16 / 4, q = l % 4;  // tile q of dims 64j + 16c ..
         uint32_t word[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            uint32_t own;  // this tile's four codes of token u, where the word's first tile has them
-            if constexpr (kInt4) {
-                own = nibbles_int4(y[u][0]) | nibbles_int4(y[u][1]) << 4 | nibbles_int4(y[u][2]) << 8 | nibbles_int4(y[u][3]) << 12;
-            } else {
-                own = bytes_e2m1(make_float2(y[u][0], 0.f), make_float2(y[u][1], 0.f), make_float2(y[u][2], 0.f), make_float2(y[u][3], 0.f));
-            }
-            constexpr int kSecond = kInt4 ? 16 : 4;
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-            word[u] = q % 2 == 0 ? own | other << kSecond : other | own << kSecond;
+            uint32_t own, other;  // this tile's four codes of token u, where the word's first tile has them; the other's
+            if constexpr (kInt4) own = four_int4(y[u][0].x, y[u][0].y, y[u][1].x, y[u][1].y);
+            else own = bytes_e2m1(make_float2(y[u][0].x, 0.f), make_float2(y[u][0].y, 0.f), make_float2(y[u][1].x, 0.f), make_float2(y[u][1].y, 0.f));
+            other = __shfl_xor_sync(D == 128 ? 0xffffffffu : 0x0000ffffu, own, 1);  // (d = 64: the lanes that take K)
+            if constexpr (kInt4) word[u] = q % 2 == 0 ? __byte_perm(own, other, 0x5410) : __byte_perm(other, own, 0x5410);
+            else word[u] = q % 2 == 0 ? own | other << 4 : other | own << 4;
         }
         // of the two words w = q/2 of tokens 2t + i, this lane stores those of t = q%2
         uint8_t *to = dst + j * 128 + c * 16 + (q % 2) * 8 + (q / 2) * 4;
@@ -209,16 +248,12 @@ __device__ __forceinline__ void code_rows4(const float4 (&r)[4], int l, bool is_
         uint32_t word[2];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            if constexpr (kInt4) {
-                word[w] = 0;
-#pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    word[w] |= nibbles_int4(y[2 * (p % 2)][2 * w + p / 2]) << (4 * p) |
-                               nibbles_int4(y[2 * (p % 2) + 1][2 * w + p / 2]) << (4 * p + 16);
-            } else {
-                word[w] = bytes_e2m1(make_float2(y[0][2 * w], y[1][2 * w]), make_float2(y[2][2 * w], y[3][2 * w]),
-                                     make_float2(y[0][2 * w + 1], y[1][2 * w + 1]), make_float2(y[2][2 * w + 1], y[3][2 * w + 1]));
-            }
+            if constexpr (kInt4)  // tokens 0 and 2 of the word's two dims in the low half, 1 and 3 in the high one
+                word[w] = __byte_perm(four_int4(y[0][w].x, y[2][w].x, y[0][w].y, y[2][w].y),
+                                      four_int4(y[1][w].x, y[3][w].x, y[1][w].y, y[3][w].y), 0x5410);
+            else
+                word[w] = bytes_e2m1(make_float2(y[0][w].x, y[1][w].x), make_float2(y[2][w].x, y[3][w].x),
+                                     make_float2(y[0][w].y, y[1][w].y), make_float2(y[2][w].y, y[3][w].y));
         }
         const int mn = l / 8, h = l % 8;  // dims 32 mn + 4h ..
         *reinterpret_cast<uint2 *>(dst + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8) = make_uint2(word[0], word[1]);
@@ -234,7 +269,7 @@ __device__ __forceinline__ void code_rows_as(const float4 (&r)[4], int l, bool i
 }
 
 template <int D, int kFormat>
-__global__ void __launch_bounds__(kThreads) code_groups_kernel(const CodeArgs a)
+__global__ void __launch_bounds__(kThreads, is_4bit(kFormat) && D == 128 ? 5 : 0) code_groups_kernel(const CodeArgs a)
 {
     const int b = blockIdx.y;
     const int lane = threadIdx.x & 31;
@@ -289,49 +324,43 @@ __global__ void __launch_bounds__(kThreads) code_groups_kernel(const CodeArgs a)
 // Values of this lane's dims (4*l .. 4*l+3) of the four tokens of a (group, head), K or V.
 // A product of a code and its tile's scale is exact in binary32.
 
-// Two codes of a byte (e2m1), the low half first.
-__device__ __forceinline__ float2 from_e2m1(uint32_t byte)
-{
-    uint32_t h;
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(byte));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
-}
-
-template <int D, bool kInt4>
+template <int D, int F>
 __device__ __forceinline__ void read_rows4(const uint8_t *src, int l, bool is_k, float s, float4 (&r)[4])
 {
-    float y[4][4];
-    uint32_t tile;
+    if constexpr (F == QSA_CODE_INT4) s *= 8.0f;  // (see TileScale)
+    const int j = l / 16, c = l % 16 / 4, q = l % 4, mn = l / 8, h = l % 8;
+    const uint32_t tile = __ldg(src + 4 * D + (is_k ? c * (D / 16) + 4 * j + q : D / 4 + h * (D / 32) + mn));
+    const TileScale<F> ts(two_e4m3(tile * 0x101u));
+    auto value = [&](uint32_t two) { return mul2(__half22float2(*reinterpret_cast<const __half2 *>(&two)), s); };
     if (is_k) {
-        const int j = l / 16, c = l % 16 / 4, q = l % 4;
-        tile = __ldg(src + 4 * D + c * (D / 16) + 4 * j + q);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const uint8_t *word = src + j * 128 + (u % 2) * 64 + c * 16 + (u / 2) * 8 + (q / 2) * 4;
-            const uint32_t own = __ldg(reinterpret_cast<const uint32_t *>(word)) >> (q % 2 * (kInt4 ? 16 : 4));
-#pragma unroll
-            for (int p = 0; p < 4; ++p)
-                y[u][p] = kInt4 ? float(int(own >> (4 * p) & 15u) - 8) : from_e2m1(own >> (8 * p)).x;
+            // this tile's half of the word, its codes brought to where decode_word has the pairs 0 and 2
+            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + j * 128 + (u % 2) * 64 + c * 16 + (u / 2) * 8 + (q / 2) * 4));
+            uint32_t own, d[4];
+            if constexpr (F == QSA_CODE_INT4) {
+                own = q % 2 == 0 ? w : w >> 16;
+                own = (own & 0x0f0fu) | (own & 0xf0f0u) << 12;
+            } else {
+                own = (q % 2 == 0 ? w : w >> 4) & 0x0f0f0f0fu;
+                own |= own >> 4;
+            }
+            decode_word<F>(own, ts, d);
+            const float2 a = value(d[0]), b = value(d[2]);
+            r[u] = make_float4(a.x, a.y, b.x, b.y);
         }
     } else {
-        const int mn = l / 8, h = l % 8;
-        tile = __ldg(src + 4 * D + D / 4 + h * (D / 32) + mn);
         const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8));
+        uint32_t d[2][4];
+        decode_word<F>(v.x, ts, d[0]);
+        decode_word<F>(v.y, ts, d[1]);
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const uint32_t word = w == 0 ? v.x : v.y;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float2 two = kInt4 ? make_float2(float(int(word >> (4 * p) & 15u) - 8), float(int(word >> (4 * p + 16) & 15u) - 8))
-                                         : from_e2m1(word >> (8 * p));
-                y[2 * (p % 2)][2 * w + p / 2] = two.x;
-                y[2 * (p % 2) + 1][2 * w + p / 2] = two.y;
-            }
+        for (int u = 0; u < 2; ++u) {  // tokens 2u and 2u + 1
+            const float2 y0 = value(d[0][u]), y1 = value(d[0][2 + u]), y2 = value(d[1][u]), y3 = value(d[1][2 + u]);
+            r[2 * u] = make_float4(y0.x, y1.x, y2.x, y3.x);
+            r[2 * u + 1] = make_float4(y0.y, y1.y, y2.y, y3.y);
         }
     }
-    const float t = from_e4m3(tile);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) r[u] = make_float4(y[u][0] * t * s, y[u][1] * t * s, y[u][2] * t * s, y[u][3] * t * s);
 }
 
 // The number that byte u of a word of 8-bit codes stands for.
@@ -396,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) read_groups_kernel(const CodeArgs a)
         float4 r[4];
         if (there) {
             const float s = __ldg(ssrc + (is_k ? 0 : 1));
-            if constexpr (is_4bit(kFormat)) read_rows4<D, kFormat == QSA_CODE_INT4>(src, l, is_k, s, r);
+            if constexpr (is_4bit(kFormat)) read_rows4<D, kFormat>(src, l, is_k, s, r);
             else read_rows8<D, kFormat == QSA_CODE_INT8>(src, l, is_k, s, r);
         } else {
 #pragma unroll
