@@ -133,7 +133,7 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * The codes, in 4 bits times their tile scales, are exact in 16-bit floats; q and the softmax weights (each times its
  * group's V scale, in binary32) enter the products as a sum of two 16-bit floats:
  * to 2^-22 of themselves, or 2^-37 of the largest of the head's q, of the head's
- * weights in four consecutive groups of the row, where that is more.  All sums,
+ * weights in four (in 4 bits: eight) consecutive groups of the row, where that is more.  All sums,
  * maxima and outputs are binary32.  Two products have to stay below 2^128 for
  * that: scale times a head's largest |q| times a K scale, and, as a weight is up to
  * 2^8 before the division by their sum, 2^8 times the sum of a row's |v|.

@@ -40,9 +40,9 @@ extern "C" {
 #define QSA_MAX_AXES 4
 
 /* One projection of the batch's new tokens.  The row of query b starts at element
- * b*stride of `rows` and holds its heads side by side; rows may overlap nothing that
- * the call writes.  `rows` NULL: this projection is not given, and what it would
- * write stays as it is. */
+ * b*stride of `rows` and holds its heads side by side.  Rows overlap nothing that the call
+ * writes, but f32 rows of q or q_idx may be in->q or in->q_idx themselves.  `rows` NULL:
+ * this projection is not given, and what it would write stays as it is. */
 typedef struct {
     const void *rows;            /* 16-byte aligned                                             */
     int64_t stride;              /* elements; at least heads*width, and 16 bytes' worth a multiple */
@@ -89,8 +89,8 @@ typedef struct {
  *
  * Everything after the load is binary32; the angle is kept as a fraction of a full turn
  * to 2^-32 whatever the position, so far positions lose nothing, and its sine and cosine
- * are off by at most 2^-22.  The sum of a head's squares has to stay below 2^128.  A
- * frequency that is not finite or not below 2^16 in size makes its pair NaN.
+ * are off by at most 2^-22.  The sum of a head's squares has to stay below 2^128, and with
+ * eps = 0 above 2^-126 (a head of zeros is NaN then).  A frequency that is not finite or not below 2^16 in size makes its pair NaN.
  * T_b = 0: the query has no new token, and nothing of it is written.  A T_b outside
  * [0, max_visible] gives zero rows in in->q and in->q_idx and no other
  * (QSA_DEVERR_VISIBLE_RANGE), a slot outside [0, num_slots) no K/V row

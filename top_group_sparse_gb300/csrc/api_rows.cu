@@ -77,7 +77,7 @@ qsa_status qsa_append_tokens(const qsa_dims *dims, const qsa_inputs *in, const q
     const qsa_status st = check_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
     if (dims->batch == 0) return QSA_OK;
-    a.positions = t.positions;
+    a.positions = a.family[0].dims + a.family[1].dims > 0 ? t.positions : nullptr;  // (read only where something turns)
     a.visible = in->visible;
     a.slot_map = in->slot_map;
     a.slot_offset = in->slot_offset;

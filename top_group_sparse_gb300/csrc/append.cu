@@ -127,7 +127,8 @@ __device__ __forceinline__ Position position_of(const AppendArgs &a, int b)
 {
     Position r;
 #pragma unroll
-    for (int x = 0; x < QSA_MAX_AXES; ++x) r.at[x] = x < a.axes && b < a.batch ? __ldg(a.positions + int64_t(x) * a.batch + b) : 0;
+    for (int x = 0; x < QSA_MAX_AXES; ++x)
+        r.at[x] = a.positions != nullptr && x < a.axes && b < a.batch ? __ldg(a.positions + int64_t(x) * a.batch + b) : 0;
     return r;
 }
 

@@ -29,20 +29,6 @@ struct Sm {
     float wm[kWarps][8 * HS], wl[kWarps][8 * HS];
 };
 
-// What the largest weight so far of a head is brought to (its log2), and by how much a weight may
-// pass that: weights stay below 2^(10 + 4 + 1 + 1/2), and keep 22 bits down to 2^-13 of the largest.
-constexpr int kWeightBits = 10, kWeightLag = 4;
-
-// The power of two for that, and its inverse.  z: log2 of the largest weight, less than 1 below.
-// (The sum with 1.5 * 2^23 rounds z to an integer and holds it in its low bits.)
-__device__ __forceinline__ void scale_of_largest(float z, float &f, float &inv)
-{
-    const uint32_t e = __float_as_uint(__fadd_rn(fmaxf(z, -110.0f), 12582912.0f));
-    const uint32_t bits = (uint32_t(kWeightBits + 127) << 23) - (e << 23);
-    f = __uint_as_float(bits);
-    inv = __uint_as_float((uint32_t(2 * 127) << 23) - bits);
-}
-
 // CTAs per SM that the registers and the ring leave room for.
 template <int D, int HS>
 constexpr int ctas_per_sm() { return HS == 2 ? 3 : D == 128 ? 4 : 6; }
@@ -252,14 +238,11 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
     // the accumulator: dims 32*j + 8*i4 + u (x) and + 4 (y) of head hl + 8*s
     float2 acc[HS][kVC][4];
     float m_run[HS], l_run[HS];
-    // what scores are kept relative to (m_run, or 0 while that is -inf) and the power of two
-    // of the weights, which follows the largest so far
-    float mref[HS], m_pass[HS], z_pass[HS], wscale[HS], winv[HS];
+    float mref[HS], m_pass[HS];  // what scores are taken relative to (m_run, or 0 while that is -inf); what none may pass
 #pragma unroll
     for (int s = 0; s < HS; ++s) {
-        m_run[s] = m_pass[s] = z_pass[s] = -INFINITY;
+        m_run[s] = m_pass[s] = -INFINITY;
         l_run[s] = mref[s] = 0.0f;
-        scale_of_largest(z_pass[s], wscale[s], winv[s]);
 #pragma unroll
         for (int j = 0; j < kVC; ++j)
 #pragma unroll
@@ -349,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                 for (int v = 0; v < kSub; ++v)
 #pragma unroll
                     for (int s = 0; s < HS; ++s) {
-                        const float f = hscale[s] * meta[v].x, from = meta[v].w - mref[s];  // (meta.w: -inf where there is no group)
+                        const float f = hscale[s] * meta[v].x;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             float2 y;
@@ -360,35 +343,25 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
 #pragma unroll
                                 for (int n = 1; n < kChains; ++n) y = add2(y, make_float2(c[v][t][n][2 * s], c[v][t][n][2 * s + 1]));
                             }
-                            x[s][v][t] = fma2s(y, f, from);
+                            x[s][v][t] = fma2s(y, f, meta[v].w);  // meta.w: -inf where there is no group
                         }
                     }
             }
 
             // ---- softmax of this lane's heads over the step, relative to mref ------------------
-            // The references follow the largest score, and the largest weight, only when those
-            // pass them by more than 2^kLag and 2^kWeightLag, so that the accumulators are rescaled a
-            // few times in a row and not at almost every step; and no lane needs to know the
-            // others' scores until one passes.
+            // The reference follows the largest score only when that passes it by more than
+            // 2^kLag, so that the accumulators are rescaled a few times in a row and not at almost
+            // every step, and no lane needs to know the others' scores until one passes.
             uint32_t ph[HS][kSub][2], pl[HS][kSub][2];
-            float xl[HS][kSub] = {}, gsum[HS][kSub];
-            auto largest_weight = [&](int s) {  // its log2, but for less than 1
-                float z = xl[s][0] + meta[0].z;
-#pragma unroll
-                for (int v = 1; v < kSub; ++v) z = fmaxf(z, xl[s][v] + meta[v].z);
-                return z;
-            };
+            float xl[HS][kSub], gsum[HS][kSub], winv[HS];
             bool passed = false;
 #pragma unroll
-            for (int s = 0; s < HS; ++s) {
-                float mc = -INFINITY;
+            for (int s = 0; s < HS; ++s)
 #pragma unroll
                 for (int v = 0; v < kSub; ++v) {
                     xl[s][v] = fmaxf(fmaxf(x[s][v][0].x, x[s][v][0].y), fmaxf(x[s][v][1].x, x[s][v][1].y));
-                    mc = fmaxf(mc, xl[s][v]);
+                    passed = passed || xl[s][v] > m_pass[s];
                 }
-                passed = passed || mc > m_pass[s] || largest_weight(s) > z_pass[s];
-            }
             if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
                 for (int s = 0; s < HS; ++s) {
@@ -397,21 +370,11 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                     for (int v = 1; v < kSub; ++v) mc = fmaxf(mc, xl[s][v]);
                     mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, 1));
                     mc = fmaxf(mc, __shfl_xor_sync(0xffffffffu, mc, 2));
-                    const float up = mc > m_pass[s] ? mc : 0.0f;  // (relative to mref)
-                    const float alpha = m_run[s] == -INFINITY ? 1.0f : ex2(-up);  // (all sums are 0 before)
-                    if (mc > m_pass[s]) m_run[s] = mref[s] += up, m_pass[s] = float(kLag);
-#pragma unroll
-                    for (int v = 0; v < kSub; ++v) {
-                        xl[s][v] -= up;
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) x[s][v][t] = add2(x[s][v][t], make_float2(-up, -up));
-                    }
-                    float z = largest_weight(s);
-                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 1));
-                    z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
-                    z = fmaxf(z_pass[s] - float(kWeightLag) - up, z);
-                    z_pass[s] = z + float(kWeightLag);
-                    scale_of_largest(z, wscale[s], winv[s]);
+                    if (!(mc > m_pass[s])) mc = m_run[s];
+                    const float alpha = mc == -INFINITY ? 1.0f : ex2(m_run[s] - mc);
+                    m_run[s] = mc;
+                    mref[s] = mc == -INFINITY ? 0.0f : mc;
+                    m_pass[s] = mc + float(kLag);
                     l_run[s] *= alpha;
 #pragma unroll
                     for (int j = 0; j < kVC; ++j)
@@ -421,13 +384,21 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
             }
 #pragma unroll
             for (int s = 0; s < HS; ++s) {
+                // the largest log2 of a weight plus exponent of a V scale
+                float zm = (xl[s][0] - mref[s]) + meta[0].z, wscale;
+#pragma unroll
+                for (int v = 1; v < kSub; ++v) zm = fmaxf(zm, (xl[s][v] - mref[s]) + meta[v].z);
+                zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 1));
+                zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 2));
+                scale_of_weights(zm, wscale, winv[s]);
 #pragma unroll
                 for (int v = 0; v < kSub; ++v) {
                     float2 p[2];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        p[t] = make_float2(ex2(x[s][v][t].x), ex2(x[s][v][t].y));
-                        split2(mul2(mul2(p[t], meta[v].y), wscale[s]), ph[s][v][t], pl[s][v][t]);
+                        p[t] = add2(x[s][v][t], make_float2(-mref[s], -mref[s]));
+                        p[t] = make_float2(ex2(p[t].x), ex2(p[t].y));
+                        split2(mul2(mul2(p[t], meta[v].y), wscale), ph[s][v][t], pl[s][v][t]);
                     }
                     const float2 g2 = add2(p[0], p[1]);
                     const float gs = g2.x + g2.y;
