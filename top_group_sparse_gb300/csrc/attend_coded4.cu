@@ -2,7 +2,35 @@
 // codes with a scale per 4 x 4 tile and one per (group, KV head) (include/qsa_cache.h:
 // qsa_attend_coded), with the attention that each group received.
 //
-// @@HEADER@@
+// The mathematics and the shape are those of attend_coded.cu: m16n8k16 products of q and of the
+// weights, each as hi + lo of two 16-bit floats, with codes that are exact in one -- here a code
+// times its tile's scale t, at most 7 significant bits -- and the group's scale applied to the
+// result (K) or to the weight (V).  What differs:
+//
+// Decoding.  Two codes become an operand register by one conversion (e2m1) or one masking into
+// the low bits of 1024 or 64 (int4), and one multiplication by t.  The layout has the two codes
+// of a pair where that finds them, a lane's codes side by side, and a tile in one lane.
+//
+// Steps of 8 groups (32 tokens).  Half the bytes per group halve the time that a step's fixed work
+// may take, so two products' tokens share a step's softmax, power of two and sums of values, and
+// q's operands are read from shared memory once for both (registers hold none of them).  No
+// lane compares its scores with the other lanes' until one passes the reference by 2^kLag.
+// (Steps of 4 groups with q in registers: 8 histories of 262,144 tokens 164 us instead of 153
+// at that time.)
+//
+// Bound: by the mix of its instructions, not by memory.  8 histories of 262,144 tokens (16 / 2
+// heads x 128, e2m1, 612 MB, 92 us at the copy rate): 138.5 us a call, 10 of it merge and
+// launches; from a cache that fits L2 it takes 133, without both products 111, and with
+// neither 55.  16 tokens cost a warp 64 conversions, 64 half multiplications and 32 matrix
+// instructions, which alone take 335-355 cycles of a scheduler (mma.sync 256 of them: it does 256
+// products a cycle here), and some 190 others.  int4 164 us: its decoding takes 9 instructions a word and 3
+// per tile pair for the offsets, against 8 and none.  32 ragged rows of up to 65,537 tokens, int4: 83.
+// 9 to 16 heads: twice the matrix instructions for the same codes (4 x 40,003 tokens of 16 heads
+// on one, with weights: 29, three quarters of a wave of runs).
+// Tried and not kept: a ring of three at three CTAs per SM (166 us), five CTAs with 96
+// registers (162), runs twice as long for 4 bits (no faster for the longest rows, 83 -> 92 for
+// ragged ones), 128 groups resolved at a time, heads as the slower dimension of the grid (the
+// two heads of a block read far apart: 7 us more).
 #include "attend_coded_common.cuh"
 #include "codes4.cuh"
 
@@ -433,21 +461,6 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                     pb[v][2 * t] = pl[0][v][t];  // (HS == 2)
                     pb[v][2 * t + 1] = pl[HS - 1][v][t];
                 }
-            // dims 32j + 4hl + u of the lane's groups: b[v] are the four tokens of group 4v + i4
-            auto add_values = [&](int j, int u, const uint32_t (&b)[kSub][2]) {
-                float c[4];
-                mma16816_first(c, pa[0], b[0][0], b[0][1]);
-#pragma unroll
-                for (int v = 1; v < kSub; ++v) mma16816(c, pa[v], b[v][0], b[v][1]);
-                if constexpr (HS == 1) {
-                    acc[0][j][u] = fma2(add2(make_float2(c[0], c[1]), make_float2(c[2], c[3])), winv[0], acc[0][j][u]);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < kSub; ++v) mma16816(c, pb[v], b[v][0], b[v][1]);
-                    acc[0][j][u] = fma2(make_float2(c[0], c[1]), winv[0], acc[0][j][u]);
-                    acc[HS - 1][j][u] = fma2(make_float2(c[2], c[3]), winv[HS - 1], acc[HS - 1][j][u]);
-                }
-            };
             const unsigned char *vp = blk0 + i4 * S::kBlk + 2 * D + hl * 16;
             const unsigned char *tp = blk0 + i4 * S::kBlk + 4 * D + D / 4 + hl * (D / 32);
             uint32_t tiles[kSub];
@@ -465,24 +478,39 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                     q[v] = *reinterpret_cast<const uint4 *>(vp + v * kSubGroups * S::kBlk + m * 128);
                     two[v] = two_e4m3(tiles[v] >> (16 * m));
                 }
+                // kWords words at a time: word w has dims 64m + 32(w/2) + 4hl + 2(w%2) and + 1 of the lane's groups.
+                // All products with one of the weights' operands come one after the other (up to 8 heads,
+                // with the four words of a half at once: 8 histories of 262,144 tokens 140.8 -> 138.9 us)
+                constexpr int kWords = HS == 1 ? 4 : 1;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int w0 = 0; w0 < 4; w0 += kWords) {
+                    float c[2 * kWords][4];
+                    uint32_t r[kSub][kWords][4];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {  // a word: dims 2h and 2h + 1
-                        uint32_t r[kSub][4];
+                    for (int v = 0; v < kSub; ++v) {
+                        const uint32_t word[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
 #pragma unroll
-                        for (int v = 0; v < kSub; ++v) {
-                            const uint32_t w = n == 0 ? (h == 0 ? q[v].x : q[v].y) : (h == 0 ? q[v].z : q[v].w);
-                            decode_word<F>(w, TileScale<F>(__byte_perm(two[v], 0, n == 0 ? 0x1010 : 0x3232)), r[v]);
-                        }
+                        for (int w = 0; w < kWords; ++w)
+                            decode_word<F>(word[w0 + w], TileScale<F>(__byte_perm(two[v], 0, (w0 + w) / 2 == 0 ? 0x1010 : 0x3232)), r[v][w]);
 #pragma unroll
-                        for (int d = 0; d < 2; ++d) {
-                            uint32_t b[kSub][2];
-#pragma unroll
-                            for (int v = 0; v < kSub; ++v) b[v][0] = r[v][2 * d], b[v][1] = r[v][2 * d + 1];
-                            add_values(2 * m + n, 2 * h + d, b);
+                        for (int u = 0; u < 2 * kWords; ++u) {
+                            if (v == 0) mma16816_first(c[u], pa[0], r[0][u / 2][2 * (u % 2)], r[0][u / 2][2 * (u % 2) + 1]);
+                            else mma16816(c[u], pa[v], r[v][u / 2][2 * (u % 2)], r[v][u / 2][2 * (u % 2) + 1]);
                         }
                     }
+#pragma unroll
+                    for (int u = 0; u < 2 * kWords; ++u) {
+                        const int at = 2 * w0 + u, j = 2 * m + at / 4;  // dims 32j + 4hl + at%4
+                        if constexpr (HS == 1) {
+                            acc[0][j][at % 4] = fma2(add2(make_float2(c[u][0], c[u][1]), make_float2(c[u][2], c[u][3])), winv[0], acc[0][j][at % 4]);
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < kSub; ++v) mma16816(c[u], pb[v], r[v][u / 2][2 * (u % 2)], r[v][u / 2][2 * (u % 2) + 1]);
+                            acc[0][j][at % 4] = fma2(make_float2(c[u][0], c[u][1]), winv[0], acc[0][j][at % 4]);
+                            acc[HS - 1][j][at % 4] = fma2(make_float2(c[u][2], c[u][3]), winv[HS - 1], acc[HS - 1][j][at % 4]);
+                        }
+                    }
+                }
             }
             __syncwarp();  // the slot is refilled by a later step
             slot = slot == (kRing - 1) * S::kStage ? 0 : slot + S::kStage;

@@ -18,6 +18,9 @@
 // t = e4m3(a / (c s)) and code = rn(x / (t s)) by the same quotients, t s being normal and
 // above 2^-90 where s is above 2^-80.  A word of K is two tiles of a token, so lanes exchange
 // their halves of it with their neighbours; a tile of V is 8 bytes of one lane.
+// 25,063 groups x 2 heads x 128, int4: 47 us (235 MB, 35 at the copy rate), half of the issue
+// slots; values one by one and all of them clamped 53, with 59 instead of 48 registers 50.
+// Read back: 39 us.
 #include "codes4.cuh"
 
 namespace qsa {
