@@ -23,8 +23,8 @@
 // launches; from a cache that fits L2 it takes 133, without both products 111, and with
 // neither 55.  16 tokens cost a warp 64 conversions, 64 half multiplications and 32 matrix
 // instructions, which alone take 335-355 cycles of a scheduler (mma.sync 256 of them: it does 256
-// products a cycle here), and some 190 others.  int4 164 us: its decoding takes 9 instructions a word and 3
-// per tile pair for the offsets, against 8 and none.  32 ragged rows of up to 65,537 tokens, int4: 83.
+// products a cycle here), and some 190 others.  int4 150 us: its decoding takes 9 instructions a word and 3
+// per tile pair for the offsets, against 8 and none.  32 ragged rows of up to 65,537 tokens, int4: 76.
 // 9 to 16 heads: twice the matrix instructions for the same codes (4 x 40,003 tokens of 16 heads
 // on one, with weights: 29, three quarters of a wave of runs).
 // Tried and not kept: a ring of three at three CTAs per SM (166 us), five CTAs with 96
@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
 #pragma unroll
     for (int e = 0; e < kEach; ++e) store_meta(tid + kThreads * e, my_blk[e], my_scales[e]);
     __syncthreads();
+    const Int4Base int4_base(uint32_t(a.batch >> 31));
     float hscale[HS];
 #pragma unroll
     for (int s = 0; s < HS; ++s) hscale[s] = a.scale * kLog2e * sm.qs[hl + 8 * s];
@@ -334,8 +335,8 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
 #pragma unroll
                         for (int v = 0; v < kSub; ++v) {
                             const TileScale<F> ts(two_e4m3(tiles[v][j] >> (16 * w)));
-                            decode_word<F>(w == 0 ? q[v].x : q[v].y, ts, r[v][0]);
-                            decode_word<F>(w == 0 ? q[v].z : q[v].w, ts, r[v][1]);
+                            decode_word<F>(w == 0 ? q[v].x : q[v].y, ts, int4_base, r[v][0]);
+                            decode_word<F>(w == 0 ? q[v].z : q[v].w, ts, int4_base, r[v][1]);
                         }
 #pragma unroll
                         for (int d = 0; d < 2; ++d)
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                         const uint32_t word[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
 #pragma unroll
                         for (int w = 0; w < kWords; ++w)
-                            decode_word<F>(word[w0 + w], TileScale<F>(__byte_perm(two[v], 0, (w0 + w) / 2 == 0 ? 0x1010 : 0x3232)), r[v][w]);
+                            decode_word<F>(word[w0 + w], TileScale<F>(__byte_perm(two[v], 0, (w0 + w) / 2 == 0 ? 0x1010 : 0x3232)), int4_base, r[v][w]);
 #pragma unroll
                         for (int u = 0; u < 2 * kWords; ++u) {
                             if (v == 0) mma16816_first(c[u], pa[0], r[0][u / 2][2 * (u % 2)], r[0][u / 2][2 * (u % 2) + 1]);

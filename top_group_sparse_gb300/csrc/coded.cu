@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, is_4bit(kFormat) && D == 128 ? 5 : 0
 // A product of a code and its tile's scale is exact in binary32.
 
 template <int D, int F>
-__device__ __forceinline__ void read_rows4(const uint8_t *src, int l, bool is_k, float s, float4 (&r)[4])
+__device__ __forceinline__ void read_rows4(const uint8_t *src, int l, bool is_k, float s, const Int4Base &base, float4 (&r)[4])
 {
     if constexpr (F == QSA_CODE_INT4) s *= 8.0f;  // (see TileScale)
     const int j = l / 16, c = l % 16 / 4, q = l % 4, mn = l / 8, h = l % 8;
@@ -348,15 +348,15 @@ __device__ __forceinline__ void read_rows4(const uint8_t *src, int l, bool is_k,
                 own = (q % 2 == 0 ? w : w >> 4) & 0x0f0f0f0fu;
                 own |= own >> 4;
             }
-            decode_word<F>(own, ts, d);
+            decode_word<F>(own, ts, base, d);
             const float2 a = value(d[0]), b = value(d[2]);
             r[u] = make_float4(a.x, a.y, b.x, b.y);
         }
     } else {
         const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8));
         uint32_t d[2][4];
-        decode_word<F>(v.x, ts, d[0]);
-        decode_word<F>(v.y, ts, d[1]);
+        decode_word<F>(v.x, ts, base, d[0]);
+        decode_word<F>(v.y, ts, base, d[1]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {  // tokens 2u and 2u + 1
             const float2 y0 = value(d[0][u]), y1 = value(d[0][2 + u]), y2 = value(d[1][u]), y3 = value(d[1][2 + u]);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) read_groups_kernel(const CodeArgs a)
         float4 r[4];
         if (there) {
             const float s = __ldg(ssrc + (is_k ? 0 : 1));
-            if constexpr (is_4bit(kFormat)) read_rows4<D, kFormat>(src, l, is_k, s, r);
+            if constexpr (is_4bit(kFormat)) read_rows4<D, kFormat>(src, l, is_k, s, Int4Base(uint32_t(a.batch >> 31)), r);
             else read_rows8<D, kFormat == QSA_CODE_INT8>(src, l, is_k, s, r);
         } else {
 #pragma unroll

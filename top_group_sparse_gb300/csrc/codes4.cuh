@@ -45,18 +45,26 @@ struct TileScale {
     }
 };
 
+// What int4 codes are put into: 1024 and 64 as pairs of 16-bit floats.  A masking into a register
+// is one instruction, into a second constant two (8 histories of 262,144 tokens 164 us instead of 150), so the
+// compiler is not to know the values: `zero` is 0 and comes from a kernel's argument.
+struct Int4Base {
+    uint32_t k1024, k64;
+    __device__ __forceinline__ explicit Int4Base(uint32_t zero) : k1024(0x64006400u + zero), k64(0x54005400u + zero) {}
+};
+
 // The four pairs of a word of 4-bit codes, times their tiles' scales, as pairs of 16-bit
 // floats.  All exact: a code has at most 3 significant bits and a scale 4.
 template <int F>
-__device__ __forceinline__ void decode_word(uint32_t w, const TileScale<F> &s, uint32_t (&r)[4])
+__device__ __forceinline__ void decode_word(uint32_t w, const TileScale<F> &s, const Int4Base &base, uint32_t (&r)[4])
 {
     if constexpr (F == QSA_CODE_INT4) {
         // code + 8 in the low bits of 1024, or four bits up in 64, is 1024 + 8 + code or 64 + 8 + code
         const uint32_t v = w >> 8;
-        r[0] = fma_f16x2((w & 0x000f000fu) | 0x64006400u, s.t, s.zero);
-        r[1] = fma_f16x2((w & 0x00f000f0u) | 0x54005400u, s.t, s.zero16);
-        r[2] = fma_f16x2((v & 0x000f000fu) | 0x64006400u, s.t, s.zero);
-        r[3] = fma_f16x2((v & 0x00f000f0u) | 0x54005400u, s.t, s.zero16);
+        r[0] = fma_f16x2((w & 0x000f000fu) | base.k1024, s.t, s.zero);
+        r[1] = fma_f16x2((w & 0x00f000f0u) | base.k64, s.t, s.zero16);
+        r[2] = fma_f16x2((v & 0x000f000fu) | base.k1024, s.t, s.zero);
+        r[3] = fma_f16x2((v & 0x00f000f0u) | base.k64, s.t, s.zero16);
     } else {
         asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
             "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
