@@ -41,8 +41,9 @@ extern "C" {
 
 /* One projection of the batch's new tokens.  The row of query b starts at element
  * b*stride of `rows` and holds its heads side by side.  Rows overlap nothing that the call
- * writes, but f32 rows of q or q_idx may be in->q or in->q_idx themselves.  `rows` NULL:
- * this projection is not given, and what it would write stays as it is. */
+ * writes, but f32 rows of q or q_idx may be in->q or in->q_idx themselves, one query's behind
+ * the other's as there (stride heads*width).  `rows` NULL: this projection is not given, and
+ * what it would write stays as it is. */
 typedef struct {
     const void *rows;            /* 16-byte aligned                                             */
     int64_t stride;              /* elements; at least heads*width, and 16 bytes' worth a multiple */
@@ -97,7 +98,8 @@ typedef struct {
  * (QSA_DEVERR_SLOT_RANGE).
  * Refused (QSA_ERR_INVALID_ARG): no projection at all, a stride or an alignment other
  * than the above, v.norm, a rotation with `dims` that is not a multiple of 8 or wider than
- * the head, without frequencies or positions; QSA_ERR_UNSUPPORTED_SHAPE: d not 64 or 128
+ * the head, without frequencies or positions, rows that start where they are written to (but the
+ * f32 queries above); QSA_ERR_UNSUPPORTED_SHAPE: d not 64 or 128
  * with q, k or v given, d_I not 32 or 64 with q_idx or idx_key given.
  * Workspace: QSA_ROWS_WORKSPACE_BYTES. */
 qsa_status qsa_append_tokens(const qsa_dims *dims, const qsa_inputs *in, const qsa_new_tokens *tokens,

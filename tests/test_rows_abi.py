@@ -219,3 +219,19 @@ def test_the_plain_coding_is_within_half_a_step():
         assert (np.abs(code * unit - x) <= np.maximum(step * unit / 2 * (1 + 2.0 ** -20), short * (1 + 2.0 ** -20))).all()
         allowed = set(c4.e2m1_table()) if fmt == c4.E2M1 else set(range(-7, 8))
         assert set(np.unique(code)) <= allowed
+
+
+def test_rows_that_are_written_over(lib):
+    """Rows that start where the call writes are refused unless they are f32 queries as they will lie."""
+    R = ctypes.byref
+    none = qsa.QsaProjection(None, 0, None)
+    for kind, n in (("q", 2048), ("k", 256), ("v", 256), ("q_idx", 512), ("idx_key", 64)):
+        for type_, stride in ((0, n), (0, n + 8), (1, n), (2, n)):
+            if kind in ("q", "q_idx") and (type_, stride) == (0, n):
+                continue  # allowed: it would be enqueued
+            tok = dict({k: none for k in ("q", "k", "v", "q_idx", "idx_key")}, type=type_)
+            tok[kind] = qsa.QsaProjection(F, stride, None)
+            assert lib.qsa_append_tokens(R(_dims()), R(_inputs()), R(_tokens(**tok)), F, 256, None) == INVALID, (kind, type_, stride)
+    # (more heads than a row's element count has bits for)
+    assert lib.qsa_append_tokens(R(_dims(batch=0, q_heads=1 << 24, kv_heads=1 << 20)), R(_inputs()),
+                                 R(_tokens(q=qsa.QsaProjection(F, 1 << 31, None), k=none, v=none)), F, 256, None) == INVALID

@@ -23,12 +23,23 @@ bool add(AppendFamily &f, int i, const qsa_projection &p, int heads, int width, 
 {
     if (p.rows == nullptr) return true;
     if (!aligned(p.rows, 16) || !aligned(p.norm, 16) || !given(out, 16)) return false;
+    if (int64_t(heads) * width > (1 << 30)) return false;  // (a row's elements are counted in 32 bits)
     if (p.stride < int64_t(heads) * width || p.stride > INT64_MAX / 65536 / 4 || p.stride * elem % 16 != 0) return false;
     f.rows[i] = p.rows;
     f.stride[i] = p.stride;
     f.norm[i] = p.norm;
     f.out[i] = static_cast<float *>(const_cast<void *>(out));
     f.heads[i] = heads;
+    return true;
+}
+
+// Rows that are what is written: f32 queries that lie as they will.  Others would be overwritten before they are read.
+bool in_place_only_as_it_lies(const AppendFamily &f, int elem, int width, int batch)
+{
+    for (int k = 0; k < 3; ++k) {
+        if (f.heads[k] == 0 || f.rows[k] != f.out[k]) continue;
+        if (k != 0 || elem != 4 || (batch > 1 && f.stride[k] != int64_t(f.heads[k]) * width)) return false;
+    }
     return true;
 }
 
@@ -77,6 +88,8 @@ qsa_status qsa_append_tokens(const qsa_dims *dims, const qsa_inputs *in, const q
     const qsa_status st = check_ws(ws, ws_bytes);
     if (st != QSA_OK) return st;
     if (dims->batch == 0) return QSA_OK;
+    for (int f = 0; f < 2; ++f)
+        if (!in_place_only_as_it_lies(a.family[f], elem, f == 0 ? d : di, dims->batch)) return QSA_ERR_INVALID_ARG;
     a.positions = a.family[0].dims + a.family[1].dims > 0 ? t.positions : nullptr;  // (read only where something turns)
     a.visible = in->visible;
     a.slot_map = in->slot_map;
