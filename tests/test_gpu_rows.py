@@ -232,6 +232,15 @@ def test_rows_that_are_the_queries_themselves():
     b.check(t)
 
 
+@pytest.mark.parametrize("shape,tokens,type_name", [((1, 1, 64, 4, 32), 20011, "bf16"), ((32, 8, 128, 8, 64), 4099, "f16"),
+                                                    ((16, 2, 128, 8, 64), 6007, "f32"), ((8, 2, 64, 4, 64), 9001, "bf16")])
+def test_more_tokens_than_are_taken_at_once(shape, tokens, type_name):
+    """Several rounds of every CTA, with queries that bring nothing and ends inside a round."""
+    need_gpu()
+    visible = np.random.default_rng(5).integers(0, 4, tokens)
+    _run(_batch(visible, shape, axes=2, dims=shape[2], idx_dims=24), type_name)
+
+
 def test_a_captured_call_replays_on_another_stream():
     torch = need_gpu()
     b = _batch([5, 2, 8, 1], (16, 2, 128, 8, 64), axes=3)

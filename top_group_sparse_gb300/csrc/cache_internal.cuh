@@ -106,8 +106,8 @@ struct AppendFamily {
     int32_t heads[3];       // 0: not given
     int32_t dims, neighbours;
     const float *freq;
+    int32_t wide;                  // the launcher's: every out is 32-byte aligned
     int32_t kind_steps[3], steps;  // the launcher's: a step is 256/width heads of a projection
-    int32_t wide;           // every out is 32-byte aligned
 };
 struct AppendArgs {
     AppendFamily family[2];
