@@ -18,9 +18,10 @@
 // t = e4m3(a / (c s)) and code = rn(x / (t s)) by the same quotients, t s being normal and
 // above 2^-90 where s is above 2^-80.  A word of K is two tiles of a token, so lanes exchange
 // their halves of it with their neighbours; a tile of V is 8 bytes of one lane.
-// 25,063 groups x 2 heads x 128, int4: 47 us (235 MB, 35 at the copy rate), half of the issue
-// slots; values one by one and all of them clamped 53, with 59 instead of 48 registers 50.
-// Read back: 39 us.
+// 25,063 groups x 2 heads x 128, int4: 43 us (235 MB, 35 at the copy rate), half of the issue
+// slots; values one by one and all of them clamped 53, with 59 instead of 48 registers 50, each look-up
+// behind the check of the one before it 47.
+// Read back: 38 us; with the codes loaded where they are used 40, two groups a warp 41, 32 registers 43.
 #include "codes4.cuh"
 
 namespace qsa {
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, is_4bit(kFormat) && D == 128 ? 5 : 0
     const int lane = threadIdx.x & 31;
     wait_for_predecessor();
     const int g_begin = __ldg(a.group_begin + b), g_end = __ldg(a.group_end + b);
+    const int64_t block_offset = __ldg(a.block_offset + b), slot_offset = __ldg(a.slot_offset + b);
     if (g_begin < 0 || g_end < g_begin || g_end > a.g_max || g_end - g_begin > a.max_groups) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, QSA_DEVERR_VISIBLE_RANGE);
         return;
@@ -287,12 +289,8 @@ __global__ void __launch_bounds__(kThreads, is_4bit(kFormat) && D == 128 ? 5 : 0
     const int h = int(item - gi * a.kv_heads);
     if (gi >= g_end - g_begin) return;
     const int64_t g = g_begin + gi;
-    const int blk = __ldg(a.block_map + __ldg(a.block_offset + b) + g);
-    if (blk < 0 || blk >= a.num_blocks) {
-        if (lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
-        return;
-    }
-    const int32_t *smap = a.slot_map + __ldg(a.slot_offset + b) + 4 * g;
+    const int blk = __ldg(a.block_map + block_offset + g);
+    const int32_t *smap = a.slot_map + slot_offset + 4 * g;
     int64_t row[4];  // element offset of each token's row, -1 for a slot outside the cache
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -300,6 +298,10 @@ __global__ void __launch_bounds__(kThreads, is_4bit(kFormat) && D == 128 ? 5 : 0
         const bool ok = slot >= 0 && slot < a.num_slots;
         if (!ok && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
         row[u] = ok ? (int64_t(slot) * a.kv_heads + h) * D : -1;
+    }
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
+        return;
     }
     uint8_t *dst = a.codes + (int64_t(blk) * a.kv_heads + h) * code_bytes(kFormat, D);
     float *sdst = a.scales + (int64_t(blk) * a.kv_heads + h) * 2;
@@ -327,43 +329,36 @@ __global__ void __launch_bounds__(kThreads, is_4bit(kFormat) && D == 128 ? 5 : 0
 // Values of this lane's dims (4*l .. 4*l+3) of the four tokens of a (group, head), K or V.
 // A product of a code and its tile's scale is exact in binary32.
 
+// What a lane loads for them.
+struct Loaded {
+    uint32_t w[4], tile;
+    float s;
+};
+
 template <int D, int F>
-__device__ __forceinline__ void read_rows4(const uint8_t *src, int l, bool is_k, float s, const Int4Base &base, float4 (&r)[4])
+__device__ __forceinline__ Loaded load_codes(const uint8_t *src, const float *scales, int l, bool is_k)
 {
-    if constexpr (F == QSA_CODE_INT4) s *= 8.0f;  // (see TileScale)
-    const int j = l / 16, c = l % 16 / 4, q = l % 4, mn = l / 8, h = l % 8;
-    const uint32_t tile = __ldg(src + 4 * D + (is_k ? c * (D / 16) + 4 * j + q : D / 4 + h * (D / 32) + mn));
-    const TileScale<F> ts(two_e4m3(tile * 0x101u));
-    auto value = [&](uint32_t two) { return mul2(__half22float2(*reinterpret_cast<const __half2 *>(&two)), s); };
-    if (is_k) {
+    Loaded x{};
+    x.s = __ldg(scales + (is_k ? 0 : 1));
+    if constexpr (is_4bit(F)) {
+        const int j = l / 16, c = l % 16 / 4, q = l % 4, mn = l / 8, h = l % 8;
+        x.tile = __ldg(src + 4 * D + (is_k ? c * (D / 16) + 4 * j + q : D / 4 + h * (D / 32) + mn));
+        if (is_k) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            // this tile's half of the word, its codes brought to where decode_word has the pairs 0 and 2
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + j * 128 + (u % 2) * 64 + c * 16 + (u / 2) * 8 + (q / 2) * 4));
-            uint32_t own, d[4];
-            if constexpr (F == QSA_CODE_INT4) {
-                own = q % 2 == 0 ? w : w >> 16;
-                own = (own & 0x0f0fu) | (own & 0xf0f0u) << 12;
-            } else {
-                own = (q % 2 == 0 ? w : w >> 4) & 0x0f0f0f0fu;
-                own |= own >> 4;
-            }
-            decode_word<F>(own, ts, base, d);
-            const float2 a = value(d[0]), b = value(d[2]);
-            r[u] = make_float4(a.x, a.y, b.x, b.y);
+            for (int u = 0; u < 4; ++u)
+                x.w[u] = __ldg(reinterpret_cast<const uint32_t *>(src + j * 128 + (u % 2) * 64 + c * 16 + (u / 2) * 8 + (q / 2) * 4));
+        } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8));
+            x.w[0] = v.x, x.w[1] = v.y;
         }
+    } else if (is_k) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x.w[u] = __ldg(reinterpret_cast<const uint32_t *>(src + (l / 16) * 256 + u * 64 + (l % 16) * 4));
     } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src + 2 * D + (mn / 2) * 128 + h * 16 + (mn % 2) * 8));
-        uint32_t d[2][4];
-        decode_word<F>(v.x, ts, base, d[0]);
-        decode_word<F>(v.y, ts, base, d[1]);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {  // tokens 2u and 2u + 1
-            const float2 y0 = value(d[0][u]), y1 = value(d[0][2 + u]), y2 = value(d[1][u]), y3 = value(d[1][2 + u]);
-            r[2 * u] = make_float4(y0.x, y1.x, y2.x, y3.x);
-            r[2 * u + 1] = make_float4(y0.y, y1.y, y2.y, y3.y);
-        }
+        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + 4 * D + l * 16));
+        x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
     }
+    return x;
 }
 
 // The number that byte u of a word of 8-bit codes stands for.
@@ -373,34 +368,65 @@ __device__ __forceinline__ float from_byte(uint32_t word, int u)
     return kInt8 ? float(int8_t(word >> (8 * u))) : from_e4m3(word >> (8 * u) & 0xffu);
 }
 
-template <int D, bool kInt8>
-__device__ __forceinline__ void read_rows8(const uint8_t *src, int l, bool is_k, float s, float4 (&r)[4])
+template <int F>
+__device__ __forceinline__ void values_of(const Loaded &x, int l, bool is_k, const Int4Base &base, float4 (&r)[4])
 {
-    if (is_k) {
+    if constexpr (is_4bit(F)) {
+        const float s = F == QSA_CODE_INT4 ? x.s * 8.0f : x.s;  // (see TileScale)
+        const TileScale<F> ts(two_e4m3(x.tile * 0x101u));
+        auto value = [&](uint32_t two) { return mul2(__half22float2(*reinterpret_cast<const __half2 *>(&two)), s); };
+        if (is_k) {
+            const int q = l % 4;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(src + (l / 16) * 256 + u * 64 + (l % 16) * 4));
-            r[u] = make_float4(from_byte<kInt8>(w, 0) * s, from_byte<kInt8>(w, 1) * s, from_byte<kInt8>(w, 2) * s,
-                               from_byte<kInt8>(w, 3) * s);
+            for (int u = 0; u < 4; ++u) {
+                // this tile's half of the word, its codes brought to where decode_word has the pairs 0 and 2
+                uint32_t own, d[4];
+                if constexpr (F == QSA_CODE_INT4) {
+                    own = q % 2 == 0 ? x.w[u] : x.w[u] >> 16;
+                    own = (own & 0x0f0fu) | (own & 0xf0f0u) << 12;
+                } else {
+                    own = (q % 2 == 0 ? x.w[u] : x.w[u] >> 4) & 0x0f0f0f0fu;
+                    own |= own >> 4;
+                }
+                decode_word<F>(own, ts, base, d);
+                const float2 a = value(d[0]), b = value(d[2]);
+                r[u] = make_float4(a.x, a.y, b.x, b.y);
+            }
+        } else {
+            uint32_t d[2][4];
+            decode_word<F>(x.w[0], ts, base, d[0]);
+            decode_word<F>(x.w[1], ts, base, d[1]);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {  // tokens 2u and 2u + 1
+                const float2 y0 = value(d[0][u]), y1 = value(d[0][2 + u]), y2 = value(d[1][u]), y3 = value(d[1][2 + u]);
+                r[2 * u] = make_float4(y0.x, y1.x, y2.x, y3.x);
+                r[2 * u + 1] = make_float4(y0.y, y1.y, y2.y, y3.y);
+            }
         }
     } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src + 4 * D + l * 16));
+        constexpr bool kInt8 = F == QSA_CODE_INT8;
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            r[u] = make_float4(from_byte<kInt8>(w.x, u) * s, from_byte<kInt8>(w.y, u) * s, from_byte<kInt8>(w.z, u) * s,
-                               from_byte<kInt8>(w.w, u) * s);
+        for (int u = 0; u < 4; ++u) {  // K: of token u's word, V: byte u of a dim's
+            if (is_k)
+                r[u] = make_float4(from_byte<kInt8>(x.w[u], 0) * x.s, from_byte<kInt8>(x.w[u], 1) * x.s,
+                                   from_byte<kInt8>(x.w[u], 2) * x.s, from_byte<kInt8>(x.w[u], 3) * x.s);
+            else
+                r[u] = make_float4(from_byte<kInt8>(x.w[0], u) * x.s, from_byte<kInt8>(x.w[1], u) * x.s,
+                                   from_byte<kInt8>(x.w[2], u) * x.s, from_byte<kInt8>(x.w[3], u) * x.s);
+        }
     }
 }
 
-// Bound by memory, by its stores: a warp takes one (group, head), reads its codes and
-// writes 32*d bytes of rows in whole 16-byte pieces.
+// Bound by memory, by its stores: a warp takes one (group, head), asks for all of its codes at
+// once, and writes 32*d bytes of rows in whole 16-byte pieces.
 template <int D, int kFormat>
-__global__ void __launch_bounds__(kThreads) read_groups_kernel(const CodeArgs a)
+__global__ void __launch_bounds__(kThreads, 6) read_groups_kernel(const CodeArgs a)
 {
     const int b = blockIdx.y;
     const int lane = threadIdx.x & 31;
     wait_for_predecessor();
     const int g_begin = __ldg(a.group_begin + b), g_end = __ldg(a.group_end + b);
+    const int64_t block_offset = __ldg(a.block_offset + b), slot_offset = __ldg(a.slot_offset + b);
     if (g_begin < 0 || g_end < g_begin || g_end > a.g_max || g_end - g_begin > a.max_groups) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, QSA_DEVERR_VISIBLE_RANGE);
         return;
@@ -410,40 +436,34 @@ __global__ void __launch_bounds__(kThreads) read_groups_kernel(const CodeArgs a)
     const int h = int(item - gi * a.kv_heads);
     if (gi >= g_end - g_begin) return;
     const int64_t g = g_begin + gi;
-    const int blk = __ldg(a.block_map + __ldg(a.block_offset + b) + g);
+    const int blk = __ldg(a.block_map + block_offset + g);
+    int slot[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) slot[u] = __ldg(a.slot_map + slot_offset + 4 * g + u);
     const bool there = blk >= 0 && blk < a.num_blocks;
-    if (!there && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
-    const int32_t *smap = a.slot_map + __ldg(a.slot_offset + b) + 4 * g;
-    int64_t row[4];
+    constexpr int kSides = D == 128 ? 2 : 1;  // K and V, or the one that this half of the warp takes
+    const int l = D == 128 ? lane : lane & 15;
+    Loaded x[kSides];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-        const int slot = __ldg(smap + u);
-        const bool ok = slot >= 0 && slot < a.num_slots;
-        if (!ok && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
-        row[u] = ok ? (int64_t(slot) * a.kv_heads + h) * D : -1;
+    for (int k = 0; k < kSides; ++k) {
+        x[k] = Loaded{};
+        const int64_t at = int64_t(blk) * a.kv_heads + h;
+        if (there) x[k] = load_codes<D, kFormat>(a.codes + at * code_bytes(kFormat, D), a.scales + 2 * at, l, kSides == 2 ? k == 0 : lane < 16);
     }
-    const uint8_t *src = a.codes + (int64_t(blk) * a.kv_heads + h) * code_bytes(kFormat, D);
-    const float *ssrc = a.scales + (int64_t(blk) * a.kv_heads + h) * 2;
-    auto read = [&](int l, bool is_k) {
-        float4 r[4];
-        if (there) {
-            const float s = __ldg(ssrc + (is_k ? 0 : 1));
-            if constexpr (is_4bit(kFormat)) read_rows4<D, kFormat>(src, l, is_k, s, Int4Base(uint32_t(a.batch >> 31)), r);
-            else read_rows8<D, kFormat == QSA_CODE_INT8>(src, l, is_k, s, r);
-        } else {
+    if (!there && lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) r[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+    for (int k = 0; k < kSides; ++k) {
+        const bool is_k = kSides == 2 ? k == 0 : lane < 16;
+        float4 r[4];
+        values_of<kFormat>(x[k], l, is_k, Int4Base(uint32_t(a.batch >> 31)), r);
         float *cache = const_cast<float *>(is_k ? a.k_cache : a.v_cache);
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (row[u] >= 0) *(reinterpret_cast<float4 *>(cache + row[u]) + l) = r[u];
-    };
-    if constexpr (D == 128) {
-        read(lane, true);
-        read(lane, false);
-    } else {
-        read(lane & 15, lane < 16);
+        for (int u = 0; u < 4; ++u) {
+            if (slot[u] >= 0 && slot[u] < a.num_slots)
+                *(reinterpret_cast<float4 *>(cache + (int64_t(slot[u]) * a.kv_heads + h) * D) + l) =
+                    there ? r[u] : make_float4(0.f, 0.f, 0.f, 0.f);
+            else if (lane == 0) set_error(a.err, QSA_DEVERR_SLOT_RANGE);
+        }
     }
 }
 
