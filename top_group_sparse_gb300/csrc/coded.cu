@@ -11,7 +11,7 @@
 // head).  A warp takes one (group, head); a lane holds the same dims of all four
 // tokens, so that the V word of a dim (its four tokens) and 16 bytes of V codes
 // leave from one lane, and every load is a 16-byte piece of a row.  25,063 groups
-// x 2 heads x 128: 43 us, 5.9 TB/s; with a division per value (793 instead of
+// x 2 heads x 128: 42 us, 6.1 TB/s; with a division per value (793 instead of
 // about 350 instructions per warp, 60 % of the issue slots) it was 57 us.
 //
 // In 4 bits a lane's 4 x 4 values are one tile, so a tile's scale t never leaves the lane:
