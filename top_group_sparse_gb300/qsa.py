@@ -117,7 +117,7 @@ class QsaRotation(ctypes.Structure):
 
 class QsaNewTokens(ctypes.Structure):
     """qsa_new_tokens (include/qsa_rows.h).  It holds pointers: the tensors it was made from have to live as
-    long as it is used."""
+    long as it is used.  Made by `of`, it knows their sizes, and a call whose dims need more is refused."""
     _fields_ = ([(n, QsaProjection) for n in ("q", "k", "v", "q_idx", "idx_key")] +
                 [("type", ctypes.c_int32), ("axes", ctypes.c_int32), ("positions", ctypes.c_void_p),
                  ("turn", QsaRotation), ("turn_idx", QsaRotation), ("eps", ctypes.c_float)])
@@ -136,7 +136,7 @@ class QsaNewTokens(ctypes.Structure):
         dtypes = {x.dtype for x, _ in given.values() if x is not None}
         if len(dtypes) != 1 or not dtypes <= set(types):
             raise ValueError(f"the projections have one type of float32, bfloat16 and float16, not {dtypes or 'none'}")
-        made = {}
+        made, sizes = {}, {}
         for name, (x, norm) in given.items():
             if x is None:
                 if norm is not None:
@@ -147,6 +147,7 @@ class QsaNewTokens(ctypes.Structure):
             # (the stride of a single row says nothing)
             width = x.shape[1] * (x.shape[2] if x.dim() == 3 else 1)
             made[name] = QsaProjection(_ptr(x), int(x.stride(0)) if x.shape[0] > 1 else width, _f32(name + "_norm", norm))
+            sizes[name] = (int(x.shape[0]), int(width), None if norm is None else int(norm.numel()))
         axes = 1 if positions is None or positions.dim() == 1 else int(positions.shape[0])
         if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
             raise ValueError("positions: int32, contiguous")
@@ -158,9 +159,54 @@ class QsaNewTokens(ctypes.Structure):
                 raise ValueError(f"{name} has a row for each of the {axes} axes of positions")
             return QsaRotation(_f32(name, f), 2 * int(f.shape[-1]), int(pair))
 
-        return cls(type=types[dtypes.pop()], axes=axes, positions=_ptr(positions), eps=float(eps),
+        self = cls(type=types[dtypes.pop()], axes=axes, positions=_ptr(positions), eps=float(eps),
                    turn=rotation("freq", freq, pairing),
                    turn_idx=rotation("idx_freq", idx_freq, pairing if idx_pairing is None else idx_pairing), **made)
+        self._sizes = sizes
+        self._places = {n: (x.rows, x.norm) for n, x in made.items()}, self.positions
+        self._position_row = None if positions is None else int(positions.shape[-1])
+        # what any call may ask for, so that one that asks for less is let through by a few comparisons
+        turned = self._turned()
+        least = lambda values: min((v for v in values if v is not None), default=1 << 62)
+        self._room = (least([r for r, _, _ in sizes.values()] + [self._position_row if turned else None]),
+                      self._position_row if turned and axes > 1 else None,
+                      least([n for k, (_, n, _) in sizes.items() if k == "q"]), least([n for k, (_, n, _) in sizes.items() if k in "kv"]),
+                      least([n for k, (_, n, _) in sizes.items() if k == "q_idx"]),
+                      least([n for k, (_, n, _) in sizes.items() if k == "idx_key"]),
+                      least([n for k, (_, _, n) in sizes.items() if k in "qk"]),
+                      least([n for k, (_, _, n) in sizes.items() if k in ("q_idx", "idx_key")]))
+        return self
+
+    def _turned(self):
+        return bool((self.turn.dims and (self.q.rows or self.k.rows)) or
+                    (self.turn_idx.dims and (self.q_idx.rows or self.idx_key.rows)))
+
+    def check(self, dims):
+        """Raises ValueError where a call with these dims would read past a tensor that `of` was given: fewer rows
+        or positions than the batch has queries (of several axes also more positions, which would be read from the
+        wrong places), rows shorter than their heads, norms shorter than a head.  A pointer that was put in the
+        place of such a tensor's later is taken as it is."""
+        room = getattr(self, "_room", None)
+        if room is None:
+            return
+        batch, d, di = dims.batch, dims.head_dim, dims.idx_dim
+        if (batch <= room[0] and (room[1] is None or batch == room[1]) and dims.q_heads * d <= room[2] and
+                dims.kv_heads * d <= room[3] and dims.idx_heads * di <= room[4] and di <= room[5] and d <= room[6] and di <= room[7]):
+            return
+        heads = {"q": dims.q_heads, "k": dims.kv_heads, "v": dims.kv_heads, "q_idx": dims.idx_heads, "idx_key": 1}
+        places, positions = self._places
+        for name, (rows, elements, norm) in self._sizes.items():
+            now, width = getattr(self, name), di if "idx" in name else d
+            same = now.rows == places[name][0]
+            if same and rows < batch:
+                raise ValueError(f"{name} has {rows} rows, the batch {batch} queries")
+            if same and elements < heads[name] * width:
+                raise ValueError(f"{name} has {elements} elements a row, not {heads[name]} heads of {width}")
+            if now.rows and norm is not None and now.norm == places[name][1] and norm < width:
+                raise ValueError(f"{name}_norm has {norm} weights, not {width}")
+        n = self._position_row
+        if n is not None and self.positions == positions and self._turned() and (n < batch or (self.axes > 1 and n != batch)):
+            raise ValueError(f"positions have {n} entries an axis, the batch {batch} queries")
 
 
 _lib = None
@@ -559,7 +605,9 @@ def code_bytes(fmt: int, head_dim: int) -> int:
 
 def qsa_append_tokens(dims, inputs, tokens, ws, stream=None) -> int:
     """Normalises and rotates the new token (the last visible one) of every query and writes it where `inputs`
-    points: q, q_idx, its row of idx_keys, its slot of k_cache / v_cache."""
+    points: q, q_idx, its row of idx_keys, its slot of k_cache / v_cache.  Tokens made of tensors that are too
+    small for dims raise ValueError."""
+    tokens.check(dims)
     p, n = _ws(ws)
     return _check("qsa_append_tokens", load().qsa_append_tokens(
         ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(tokens), p, n, _stream(stream)))
