@@ -182,6 +182,10 @@ __device__ __forceinline__ void make_angles(const AppendArgs &a, Table &table, c
     }
 }
 
+// All of the CTA's warps, whichever family's step each takes: they come here from different instantiations, so
+// the barrier is one with a count of threads (__syncthreads() would have to be the same one for all).  It needs
+// both to run the same number of rounds, which the batch, the tokens at a time and the grid alone decide.
+__device__ __forceinline__ void meet_all_steps() { asm volatile("barrier.cta.sync 1, %0;" ::"r"(blockDim.x) : "memory"); }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N, typename V>
 __device__ __forceinline__ void copy_async(V *to, const V *from)
@@ -243,7 +247,8 @@ __device__ __forceinline__ void look_up_slots(const AppendArgs &a, Lookup &at, i
 }
 
 // Step `step` of one family for all the CTA's tokens, a.tokens at a time: batches blockIdx.x,
-// blockIdx.x + gridDim.x, ..  Control is the same for the whole warp throughout, but for a rotation of a part of a head.
+// blockIdx.x + gridDim.x, ..  Control is the same for the whole warp throughout, but for a rotation of a part of a head,
+// and barriers and rounds are the same for both families.
 template <typename T, int D, int DI, int kFamily>
 __device__ __forceinline__ void append_step(const AppendArgs &a, Table &table, T *ring, const Angle &mine, int pairs0, int pairs, int step)
 {
@@ -312,7 +317,7 @@ __device__ __forceinline__ void append_step(const AppendArgs &a, Table &table, T
     commit();
     make_turns(a, table, pairs0, pairs);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
-    __syncthreads();
+    meet_all_steps();
     look_up_slots(a, table.lookup[0], tokens_at(first));
     make_angles<D, DI>(a, table, table.lookup[0], mine, pairs0, pairs, 0, tokens_at(first));
     while (first < a.batch) {
@@ -322,7 +327,7 @@ __device__ __forceinline__ void append_step(const AppendArgs &a, Table &table, T
         look_up(a, table.lookup[(turn + 2) % 4], next + stepped, tokens_at(next + stepped));
         commit();
         asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncthreads();
+        meet_all_steps();
         const Lookup &at = table.lookup[turn];
         look_up_slots(a, table.lookup[(turn + 1) % 4], tokens_at(next));
 #pragma unroll kTogether
