@@ -134,9 +134,12 @@ size_t qsa_coded_workspace_size(const qsa_dims *dims, int32_t whole_history, int
  * group's V scale, in binary32) enter the products as a sum of two 16-bit floats:
  * to 2^-22 of themselves, or 2^-37 of the largest of the head's q, of the head's
  * weights in four (in 4 bits: eight) consecutive groups of the row, where that is more.  All sums,
- * maxima and outputs are binary32.  Two products have to stay below 2^128 for
+ * maxima and outputs are binary32.  Three products have to stay below 2^128 for
  * that: scale times a head's largest |q| times a K scale, and, as a weight is up to
- * 2^8 before the division by their sum, 2^8 times the sum of a row's |v|.
+ * 2^8 before the division by their sum, 2^8 times the sum of a row's |v| and 2^8 times
+ * a V scale (which the one before it implies for groups that qsa_code_groups coded).
+ * Where a head's q is not all zeros, its largest |q| is at least 2^-110, and scale
+ * times that at least 2^-112.
  *
  * A count outside [0, row_cap] or a T_b outside [0, max_visible] gives a zero
  * output (QSA_DEVERR_ROW_RANGE / QSA_DEVERR_VISIBLE_RANGE) and adds no weight;

@@ -141,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                         : make_float2(0.0f, 0.0f);
     };
     auto store_meta = [&](int at, int blk, float2 sc) {
-        if constexpr (F == QSA_CODE_INT4) sc = make_float2(8.0f * sc.x, 8.0f * sc.y);  // (see TileScale)
         const uint32_t bits = __float_as_uint(sc.y) & 0x7fffffffu;
         const float e = bits == 0 ? -INFINITY : float(int(bits >> 23) - 127);
         sm.meta[at] = make_float4(sc.x, sc.y, e, blk != -1 ? 0.0f : -INFINITY);
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
     const Int4Base int4_base(uint32_t(a.batch >> 31));
     float hscale[HS];
 #pragma unroll
-    for (int s = 0; s < HS; ++s) hscale[s] = a.scale * kLog2e * sm.qs[hl + 8 * s];
+    for (int s = 0; s < HS; ++s) hscale[s] = a.scale * kLog2e * sm.qs[hl + 8 * s] * kUnits<F>;
 
     // the accumulator: dims 32*j + 8*i4 + u (x) and + 4 (y) of head hl + 8*s
     float2 acc[HS][kVC][4];
@@ -419,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, (ctas_per_sm<D, HS>())) attend_coded
                 for (int v = 1; v < kSub; ++v) zm = fmaxf(zm, (xl[s][v] - mref[s]) + meta[v].z);
                 zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 1));
                 zm = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 2));
-                scale_of_weights(zm, wscale, winv[s]);
+                scale_of_weights<kLog2Units<F>>(zm, wscale, winv[s]);
 #pragma unroll
                 for (int v = 0; v < kSub; ++v) {
                     float2 p[2];

@@ -94,12 +94,14 @@ __device__ __forceinline__ void scale_of_q(uint32_t top, float &f, float &inv)
 // a softmax weight's log2 and a V scale's exponent, so that the largest weight is
 // 2^z to 2^(z+1); at most 16 + 121, and NaN where every weight is (any power will do).
 // The sum with 1.5 * 2^23 rounds z to an integer and holds it in its low bits.
+// kLog2Units: of what the weights are multiplied with; the inverse makes up for that too.
+template <int kLog2Units = 0>
 __device__ __forceinline__ void scale_of_weights(float z, float &f, float &inv)
 {
     const uint32_t e = __float_as_uint(__fadd_rn(fmaxf(z, -110.0f), 12582912.0f));
     const uint32_t bits = (uint32_t(13 + 127) << 23) - (e << 23);
     f = __uint_as_float(bits);
-    inv = __uint_as_float((uint32_t(2 * 127) << 23) - bits);
+    inv = __uint_as_float((uint32_t(2 * 127 + kLog2Units) << 23) - bits);
 }
 
 constexpr int kLag = 8;     // log2 of the largest softmax weight (16 where the scores' own rounding is that coarse)

@@ -372,9 +372,11 @@ template <int F>
 __device__ __forceinline__ void values_of(const Loaded &x, int l, bool is_k, const Int4Base &base, float4 (&r)[4])
 {
     if constexpr (is_4bit(F)) {
-        const float s = F == QSA_CODE_INT4 ? x.s * 8.0f : x.s;  // (see TileScale)
         const TileScale<F> ts(two_e4m3(x.tile * 0x101u));
-        auto value = [&](uint32_t two) { return mul2(__half22float2(*reinterpret_cast<const __half2 *>(&two)), s); };
+        auto value = [&](uint32_t two) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&two));
+            return mul2(F == QSA_CODE_INT4 ? mul2(v, kUnits<F>) : v, x.s);
+        };
         if (is_k) {
             const int q = l % 4;
 #pragma unroll

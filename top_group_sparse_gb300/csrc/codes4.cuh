@@ -31,8 +31,8 @@ __device__ __forceinline__ uint32_t two_e4m3(uint32_t codes)  // the low two byt
 template <int F>
 struct TileScale {
     uint32_t t, zero, zero16;
-    // int4: an eighth of the scale, so that the products with 1032 and 72 stay below 2^16
-    // (the group's scale makes up for it)
+    // int4: an eighth of the scale, so that the products with 1032 and 72 stay below 2^16; kUnits makes
+    // up for it (not in the group's scale, which may be any finite number)
     __device__ __forceinline__ explicit TileScale(uint32_t pair)
     {
         if constexpr (F == QSA_CODE_INT4) {
@@ -45,6 +45,12 @@ struct TileScale {
     }
 };
 
+// What a decoded value has to be multiplied by.
+template <int F>
+constexpr int kLog2Units = F == QSA_CODE_INT4 ? 3 : 0;
+template <int F>
+constexpr float kUnits = float(1 << kLog2Units<F>);
+
 // What int4 codes are put into: 1024 and 64 as pairs of 16-bit floats.  A masking into a register
 // is one instruction, into a second constant two (8 histories of 262,144 tokens 164 us instead of 150), so the
 // compiler is not to know the values: `zero` is 0 and comes from a kernel's argument.
@@ -54,7 +60,7 @@ struct Int4Base {
 };
 
 // The four pairs of a word of 4-bit codes, times their tiles' scales, as pairs of 16-bit
-// floats.  All exact: a code has at most 3 significant bits and a scale 4.
+// floats in units of kUnits.  All exact: a code has at most 3 significant bits and a scale 4.
 template <int F>
 __device__ __forceinline__ void decode_word(uint32_t w, const TileScale<F> &s, const Int4Base &base, uint32_t (&r)[4])
 {
