@@ -89,8 +89,8 @@ typedef struct {
  * given projection needs may be NULL.  No two queries may name the same place.
  *
  * Everything after the load is binary32; the angle is kept as a fraction of a full turn
- * to 2^-32 whatever the position, so far positions lose nothing, and its sine and cosine
- * are off by at most 2^-22.  The sum of a head's squares has to stay below 2^128, and with
+ * to (axes + 3) * 2^-34 whatever the position, so far positions lose nothing, and its sine and
+ * cosine are off by at most 2^-22.  The sum of a head's squares has to stay below 2^128, and with
  * eps = 0 above 2^-126 (a head of zeros is NaN then).  A frequency that is not finite or not below 2^16 in size makes its pair NaN.
  * T_b = 0: the query has no new token, and nothing of it is written.  A T_b outside
  * [0, max_visible] gives zero rows in in->q and in->q_idx and no other

@@ -4,10 +4,11 @@
 // Mathematics.  y = x * w * (mean(x^2) + eps)^(-1/2) per head; pairs of dims turn by
 // angle_j = sum_a pos_a * freq_aj.  Far positions times binary32 frequencies lose the
 // angle's fraction of a turn in binary32, so the turns are kept in 64-bit fixed point:
-// F = freq / (2 pi) as a fraction of a turn, exact to 2^-64, is made once per CTA by an
-// integer product with 1/(2 pi), and pos * F modulo 2^64 is the angle modulo a full turn
-// for every position.  Its nearest quarter is taken off in integers, and sine and cosine of the
-// rest are short Taylor series.
+// F = freq / (2 pi) as a fraction of a turn, to half of 2^-64, is made once per CTA by an
+// integer product with 1/(2 pi), and the axes' sum of pos * F modulo 2^64 is the angle modulo a
+// full turn for every position: each F is off by 2^-65 (and the 2^-72 that its product leaves out)
+// times at most 2^31, and the sum is rounded to 2^-32 once, below (axes + 3) * 2^-34 in all.  Its
+// nearest quarter is taken off in integers, and sine and cosine of the rest are short Taylor series.
 //
 // Layout.  Partners sit in one lane: it holds eight neighbouring dims of a head's first half and
 // the eight that turn with them (neighbours, or nothing turned: of its second half), so a head is a
@@ -45,7 +46,8 @@ struct Lookup {
     int32_t position[QSA_MAX_AXES][kTokens];
 };
 struct Table {
-    uint64_t turns[2][QSA_MAX_AXES][kMaxWidth / 2];  // by family: heads of d, heads of d_I
+    // by family: heads of d, heads of d_I.  The lower half is a signed number, and the upper one makes up for that
+    uint64_t turns[2][QSA_MAX_AXES][kMaxWidth / 2];
     float norm[2][2][kMaxWidth];                     // weights of dim i at place_of(i): q, k; q_idx, idx_key
     float bad[2][kMaxWidth / 2];                     // NaN for a pair with a frequency out of range, else 0
     Lookup lookup[4];
@@ -64,7 +66,7 @@ __device__ __forceinline__ float *angles_of(Table &table, int token)
     return reinterpret_cast<float *>(&table + 1) + token * (2 * (D + DI)) + (kFamily == 0 ? 0 : 2 * D);
 }
 
-// f / (2 pi) as a fraction of a turn (modulo 1, in units of 2^-64) for |f| < 2^16.
+// f / (2 pi) as a fraction of a turn (modulo 1, in units of 2^-64, to the nearest) for |f| < 2^16.
 __device__ __forceinline__ uint64_t turns_of(float f)
 {
     const uint32_t bits = __float_as_uint(f);
@@ -75,7 +77,7 @@ __device__ __forceinline__ uint64_t turns_of(float f)
     const unsigned __int128 lo = (unsigned __int128)m * 0x7f09d5f47d4d3770ull;
     const unsigned __int128 p = (unsigned __int128)m * 0x28be60db9391054aull + (lo >> 64);
     const int shift = 23 - e;                    // 8 .. 149
-    const uint64_t t = shift < 128 ? uint64_t(p >> shift) : 0;
+    const uint64_t t = shift < 128 ? uint64_t(((p >> (shift - 1)) + 1) >> 1) : 0;
     return bits >> 31 ? 0 - t : t;
 }
 
@@ -145,14 +147,17 @@ __device__ __forceinline__ void make_angles(const AppendArgs &a, Table &table, c
         const int to = place_of(neighbours ? 2 * j : j, width);
         const float bad = table.bad[fam][j];
         for (int u = mine.u; u < n; u += mine.u_step) {
-            uint32_t phase = 0;  // the upper half of the products' sum modulo 2^64, but for the lower halves' carries
+            uint64_t low = 1u << 31;  // the products' sum modulo 2^64, rounded to its upper half: the lower halves' part
+            uint32_t phase = 0;       // .. and the upper halves'
 #pragma unroll
             for (int x = 0; x < QSA_MAX_AXES; ++x)
                 if (x < a.axes) {
                     const uint64_t t = table.turns[fam][x][j];
                     const int pos = at.position[x][u];
-                    phase += __umulhi(uint32_t(pos), uint32_t(t)) + uint32_t(pos) * uint32_t(t >> 32) - (pos < 0 ? uint32_t(t) : 0u);
+                    low += uint64_t(int64_t(pos) * int32_t(t));
+                    phase += uint32_t(pos) * uint32_t(t >> 32);
                 }
+            phase += uint32_t(low >> 32);
             // in integers to the nearest quarter of a turn; of the rest x, at most pi/4 in size, the Taylor series
             // to x^9 and x^8 (what is left out is below 2e-9 and 3e-8)
             const uint32_t quarter = (phase + (1u << 29)) >> 30;
@@ -215,7 +220,8 @@ __device__ __forceinline__ void make_turns(const AppendArgs &a, Table &table, in
         for (int x = 0; x < a.axes; ++x) {
             const float now = x == 0 ? f[0] : x == 1 ? f[1] : x == 2 ? f[2] : f[3];
             const bool ok = fabsf(now) < 65536.0f;
-            table.turns[fam][x][j] = ok ? turns_of(now) : 0;
+            const uint64_t t = ok ? turns_of(now) : 0;
+            table.turns[fam][x][j] = t + ((t & 0x80000000u) << 1);
             if (!ok) bad = __int_as_float(0x7fffffff);
         }
         table.bad[fam][j] = bad;
