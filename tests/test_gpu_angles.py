@@ -81,3 +81,42 @@ def test_the_fraction_of_a_turn_whatever_the_position(axes):
         err = abs(float(sine[b, j]) - np.sin(angle)) / rh.TWO_PI
         worst = max(worst, (err - 4 * 2.0 ** -24 * abs(turn)) * 2.0 ** 34)
     assert worst <= axes + 3, worst
+
+
+@pytest.mark.parametrize("pairing", [rh.HALVES, rh.NEIGHBOURS])
+@pytest.mark.parametrize("far", [1000, 2 ** 31])
+def test_sines_and_cosines_to_two_to_the_minus_22(far, pairing):
+    """64,000 angles all over the turn."""
+    need_gpu()
+    r = np.random.RandomState(3)
+    freq = np.exp(r.uniform(np.log(0.01), np.log(100.0), (1, 32))).astype(np.float32)
+    positions = r.randint(-far, far, (1, 2000), dtype=np.int64).astype(np.int32)
+    c, s = _read_out(positions, freq, pairing)
+    want = rh.angles(positions, freq)
+    assert np.abs(c - np.cos(want)).max() <= 2.0 ** -22
+    assert np.abs(s - np.sin(want)).max() <= 2.0 ** -22
+    # the whole of a turn's quarters, their ends among them
+    x = np.abs(want / rh.TWO_PI * 4 - np.rint(want / rh.TWO_PI * 4))
+    assert x.max() > 0.4999 and x.min() < 1e-4
+
+
+@pytest.mark.parametrize("type_name", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("pairing", [rh.HALVES, rh.NEIGHBOURS])
+@pytest.mark.parametrize("dims,idx_dims", [(128, 64), (72, 40), (16, 8), (24, 56)])
+def test_turned_rows_without_norms(dims, idx_dims, pairing, type_name):
+    """A turned element is two products with a sine and a cosine that are off by 2^-22, and their sum: 6 * 2^-24 of
+    |y_i| + |y_k| (rows_helpers derives it), a quarter of what that allows where a norm may come before it."""
+    need_gpu()
+    from top_group_sparse_gb300 import qsa
+    b = rh.Batch([7, 3, 1, 0, 20], q_heads=6, kv_heads=2, head_dim=128, idx_heads=5, idx_dim=64, seed=5, norms=False, dims=dims,
+                 idx_dims=idx_dims, pairing=pairing, axes=3, far=1 << 30)
+    t = b.on_device(type_name)
+    qsa.qsa_append_tokens(t["dims"], t["inputs"], t["tokens"], t["ws"])
+    assert qsa.qsa_check_errors(t["ws"]) == (0, 0)
+    want = b.expected(type_name)
+    has, row, slot = b.places()
+    for kind, name, at in (("q", "q", np.flatnonzero(has)), ("k", "k_cache", slot), ("q_idx", "q_idx", np.flatnonzero(has)),
+                           ("idx_key", "idx_keys", row)):
+        y, tol = want[kind]
+        got = t[name].cpu().numpy().reshape(t[name].shape[0], -1, b.width[kind])[at].astype(np.float64)
+        assert (np.abs(got - y[has]) <= tol[has] / 4).all(), kind
