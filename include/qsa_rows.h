@@ -90,8 +90,9 @@ typedef struct {
  *
  * Everything after the load is binary32; the angle is kept as a fraction of a full turn
  * to (axes + 3) * 2^-34 whatever the position, so far positions lose nothing, and its sine and
- * cosine are off by at most 2^-22.  The sum of a head's squares has to stay below 2^128, and with
- * eps = 0 above 2^-126 (a head of zeros is NaN then).  A frequency that is not finite or not below 2^16 in size makes its pair NaN.
+ * cosine are off by at most 2^-22.  The sum of a head's squares has to stay below 2^128; it may be
+ * as small as it likes, but for a head of zeros, which with eps = 0 is NaN.  A frequency that
+ * is not finite or not below 2^16 in size makes its pair NaN.
  * T_b = 0: the query has no new token, and nothing of it is written.  A T_b outside
  * [0, max_visible] gives zero rows in in->q and in->q_idx and no other
  * (QSA_DEVERR_VISIBLE_RANGE), a slot outside [0, num_slots) no K/V row

@@ -349,13 +349,23 @@ __device__ __forceinline__ void append_step(const AppendArgs &a, Table &table, T
                 for (int i = 0; i < 4; ++i) widen<T, 4>(row + dim_of(i), x + 2 * i);
             }
             if (normed) {
-                float2 sq = mul2(x[0], x[0]);
+                auto mean_square = [&](float eps) {
+                    float2 sq = mul2(x[0], x[0]);
 #pragma unroll
-                for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
-                float ss = sq.x + sq.y;
+                    for (int i = 1; i < 8; ++i) sq = fma2(x[i], x[i], sq);
+                    float ss = sq.x + sq.y;
 #pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float r = rsqrtf(fmaf(ss, 1.0f / W, a.eps));
+                    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    return fmaf(ss, 1.0f / W, eps);
+                };
+                float mean = mean_square(a.eps);
+                if (__any_sync(0xffffffffu, mean < 0x1p-100f)) {  // squares that lose bits, or all of them: of 2^96 x
+                    const float up = mean < 0x1p-100f ? 0x1p96f : 1.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], make_float2(up, up));
+                    mean = mean_square(a.eps * up * up);
+                }
+                const float r = rsqrtf(mean);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int at = beside ? (e + i / 2 * apart) / 2 + i % 2 * (kMaxWidth / 2) : place_of(dim_of(i), kMaxWidth);
