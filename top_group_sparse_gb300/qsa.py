@@ -895,8 +895,19 @@ class DeviceBatch:
         self.weights = torch.zeros(max(weights, 1), dtype=torch.float32, device=dev)
         self.coded = QsaCodedCache.of(self.codes, self.scales, self.block_map, self.block_offset, fmt)
         self.coded_ws = torch.zeros(qsa_coded_workspace_size(self.dims, True, True), dtype=torch.uint8, device=dev)
-        self._code_owner = np.array([owner[k] == b for b, k in enumerate(ko.tolist())])
+        self._code_history = np.unique(ko, return_inverse=True)[1].reshape(-1)
         return self.coded
+
+    def _whole_histories(self):
+        """Group ends per query that cover every complete group of each history once, as the batch stands: at the first
+        of the queries that see most of it."""
+        T, of = self.visible.cpu().numpy(), self._code_history
+        order = np.lexsort((np.arange(len(T)), -T.astype(np.int64), of))
+        first = order[np.r_[True, of[order][1:] != of[order][:-1]]] if len(T) else order
+        ge = np.zeros(len(T), np.int32)
+        ge[first] = T[first] // 4
+        ge[T < 0] = -1  # (the call flags it)
+        return ge
 
     def code(self, group_begin, group_end, stream=None):
         """Codes groups [group_begin[b], group_end[b]) of every query (host arrays, copied on `stream`:
@@ -915,7 +926,7 @@ class DeviceBatch:
     def read_back(self, stream=None):
         """Writes every complete group of every history from its codes back to its rows of k_cache / v_cache."""
         import torch
-        ge = np.where(self._code_owner, self.visible.cpu().numpy() // 4, 0).astype(np.int32)
+        ge = self._whole_histories()
         handle = _stream(stream)
         on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
         with torch.cuda.stream(on):
@@ -925,7 +936,7 @@ class DeviceBatch:
 
     def code_all(self, stream=None):
         """Codes every complete group of every history (once per history)."""
-        ge = np.where(self._code_owner, self.visible.cpu().numpy() // 4, 0).astype(np.int32)
+        ge = self._whole_histories()
         return self.code(np.zeros_like(ge), ge, stream)
 
     def attend_coded(self, whole=False, weigh=False, stream=None):
