@@ -577,8 +577,7 @@ cudaError_t launch_t(const AttendCodedArgs &a, int runs, cudaStream_t s)
 {
     using S = Sm<D, HS, F>;
     static_assert(sizeof(S) <= 227 * 1024, "shared memory per CTA");
-    static_assert(ctas_per_sm<D, HS>() * (sizeof(S) + 1024) <= 228 * 1024 || (D == 64 && HS == 2),
-                  "the CTAs per SM that the kernels are built for");
+    static_assert(ctas_per_sm<D, HS>() * (sizeof(S) + 1024) <= 228 * 1024, "the CTAs per SM that the kernels are built for");
     static_assert(kSegGroups % kThreads == 0, "groups that a thread resolves");
     static_assert(kWarps * 8 * HS * D * 4 <= int(sizeof(S::ring)), "the reduction area fits the ring");
     const size_t smem = sizeof(S);
