@@ -18,12 +18,15 @@
 // (Steps of 4 groups with q in registers: 8 histories of 262,144 tokens 164 us instead of 153
 // at that time.)
 //
-// Bound: by the mix of its instructions, not by memory.  8 histories of 262,144 tokens (16 / 2
+// Bound: by the latency of a warp's own chain (copy wait, shared loads, decoding, dependent products, softmax with two
+// shuffles, split, products), four warps to a scheduler, not by memory and not by a pipe.  8 histories of 262,144 tokens (16 / 2
 // heads x 128, e2m1, 612 MB, 92 us at the copy rate): 138.5 us a call, 10 of it merge and
 // launches; from a cache that fits L2 it takes 133, without both products 111, and with
 // neither 55.  16 tokens cost a warp 64 conversions, 64 half multiplications and 32 matrix
 // instructions, which alone take 335-355 cycles of a scheduler (mma.sync 256 of them: it does 256
-// products a cycle here), and some 190 others.  int4 150 us: its decoding takes 9 instructions a word and 3
+// products a cycle here), and some 190 others; the kernel takes 618, with half of the issue slots and 36 % of the
+// tensor pipe used, and 11 instructions a step less measured the same.  Nothing here starts the scores of the next
+// step before the values of this one.  int4 150 us: its decoding takes 9 instructions a word and 3
 // per tile pair for the offsets, against 8 and none.  32 ragged rows of up to 65,537 tokens, int4: 76.
 // 9 to 16 heads: twice the matrix instructions for the same codes (4 x 40,003 tokens of 16 heads
 // on one, with weights: 29, three quarters of a wave of runs).
