@@ -39,6 +39,38 @@ def test_the_ends_of_histories_of_their_own():
         assert db._whole_histories().tolist() == want and db._whole_histories().dtype == np.int32
 
 
+def test_groups_without_a_block_are_refused(monkeypatch):
+    """A history that has grown past the blocks it was given: its next entries of the block map are another
+    history's, or past the end."""
+    from top_group_sparse_gb300 import build
+    build.build()
+    calls = []
+    for name in ("qsa_code_groups", "qsa_read_groups"):
+        monkeypatch.setattr(qsa, name, lambda *a: calls.append(a[3:6]))
+    monkeypatch.setattr(qsa, "_stream", lambda stream: 0)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda: None)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: __import__("contextlib").nullcontext())
+    db = qsa.DeviceBatch(_workload([40, 40, 40], "independent"), device="cpu")
+    db.visible.copy_(torch.tensor([20, 11, 40], dtype=torch.int32))
+    db.make_coded_cache()
+    for grown, bad in (([24, 11, 40], 0), ([20, 12, 40], 1), ([23, 40, 8], 1)):
+        db.visible.copy_(torch.tensor(grown, dtype=torch.int32))
+        ge = np.array(grown) // 4
+        for call in (db.code_all, db.read_back, lambda: db.code(ge - 1, ge)):
+            with pytest.raises(ValueError, match=f"query {bad}: groups up to {ge[bad]} "):
+                call()
+    assert not calls
+    db.visible.copy_(torch.tensor([23, 8, 40], dtype=torch.int32))
+    db.code_all()
+    db.read_back()
+    db.code([0, 9, 10], [5, 9, 10])          # (an empty range anywhere)
+    assert [(lo.tolist(), hi.tolist(), n) for lo, hi, n in calls] == [([0, 0, 0], [5, 2, 10], 10)] * 2 + [([0, 9, 10], [5, 9, 10], 5)]
+    db.visible.copy_(torch.tensor([40, 40, 40], dtype=torch.int32))
+    db.coded = qsa.QsaCodedCache.of(db.codes, db.scales, db.block_map, db.block_offset, 0)  # the caller's own: not looked into
+    db.code_all()
+    assert calls[-1][2] == 10
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", [qsa.QSA_CODE_E4M3, qsa.QSA_CODE_INT4])
 def test_a_history_whose_longest_query_is_another_one(fmt):

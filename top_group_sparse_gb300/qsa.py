@@ -871,7 +871,8 @@ class DeviceBatch:
     def make_coded_cache(self, fmt=QSA_CODE_E4M3):
         """Allocates the coded cache: one block per complete group of each distinct
         history (in order), its accumulated weights (one per group and one for an
-        incomplete one) and a workspace that serves every call on this batch."""
+        incomplete one) and a workspace that serves every call on this batch.  Histories
+        that are to grow are as long as they will be when this is called."""
         import torch
         ko = self.key_offset.cpu().numpy()
         T = self.visible.cpu().numpy()
@@ -896,7 +897,19 @@ class DeviceBatch:
         self.coded = QsaCodedCache.of(self.codes, self.scales, self.block_map, self.block_offset, fmt)
         self.coded_ws = torch.zeros(qsa_coded_workspace_size(self.dims, True, True), dtype=torch.uint8, device=dev)
         self._code_history = np.unique(ko, return_inverse=True)[1].reshape(-1)
+        self._code_room = np.array([int(T[owner[k]]) // 4 for k in ko.tolist()], np.int32), self.coded
         return self.coded
+
+    def _check_blocks(self, group_begin, group_end):
+        """Refuses groups behind the last block of their history, whose entries of the block map are another's."""
+        room, made = self._code_room
+        if made is not self.coded:  # (a cache of the caller's own)
+            return
+        over = np.flatnonzero((group_end > group_begin) & (group_end > room))
+        if len(over):
+            b = int(over[0])
+            raise ValueError(f"query {b}: groups up to {int(group_end[b])} of a history that had blocks for {int(room[b])} "
+                             "when the cache was made")
 
     def _whole_histories(self):
         """Group ends per query that cover every complete group of each history once, as the batch stands: at the first
@@ -916,6 +929,7 @@ class DeviceBatch:
         gb, ge = np.asarray(group_begin, np.int32), np.asarray(group_end, np.int32)
         if gb.shape != (self.dims.batch,) or ge.shape != gb.shape:
             raise ValueError(f"group_begin and group_end have one entry per query ({self.dims.batch})")
+        self._check_blocks(gb, ge)
         handle = _stream(stream)
         on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
         with torch.cuda.stream(on):  # their memory is that stream's, until the next call there
@@ -927,6 +941,7 @@ class DeviceBatch:
         """Writes every complete group of every history from its codes back to its rows of k_cache / v_cache."""
         import torch
         ge = self._whole_histories()
+        self._check_blocks(np.zeros_like(ge), ge)
         handle = _stream(stream)
         on = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
         with torch.cuda.stream(on):
