@@ -62,3 +62,18 @@ def test_heads_of_zeros_beside_small_ones():
     assert (np.abs(got - want[0]) <= want[1])[keep].all()
     b.eps = 1e-40
     assert (_check(b, "f32")["q"][0, 1] == 0).all()
+
+
+def test_a_head_gives_the_same_bits_beside_small_ones():
+    torch = need_gpu()
+    make = lambda: rh.Batch([3, 4, 9, 1], q_heads=4, kv_heads=2, head_dim=64, idx_heads=4, idx_dim=32, seed=8, eps=1e-35)
+    alone, beside = make(), make()
+    beside.fused[:, 64:128] *= np.float32(2.0 ** -70)     # q head 1 alone
+    beside.fused[1] *= np.float32(2.0 ** -60)             # a token that shares its warps' turns with its neighbours
+    a, b = _check(alone, "f32"), _check(beside, "f32")
+    for name in ("q", "q_idx"):
+        same = torch.ones(4, 4, dtype=torch.bool, device="cuda")
+        same[1] = False
+        if name == "q":
+            same[:, 1] = False
+        assert torch.equal(a[name][same], b[name][same])
