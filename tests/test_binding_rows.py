@@ -85,3 +85,18 @@ def test_pointers_put_in_the_place_of_a_tensor_are_taken_as_they_are(calls):
             qsa.qsa_append_tokens(dims, qsa.QsaInputs(), t, ws, 0)
         change()
     assert qsa.qsa_append_tokens(dims, qsa.QsaInputs(), t, ws, 0) == 0 and len(calls) == 1
+
+
+def test_dims_that_change_between_calls(calls):
+    dims, ws = qsa.make_dims(B, **DIMS), torch.zeros(256, dtype=torch.uint8)
+    t = qsa.QsaNewTokens.of(**_tensors())
+    for batch, head_dim, q_heads, fits in ((B, 64, 4, True), (B, 64, 4, True), (B + 1, 64, 4, False), (B, 128, 2, False), (B, 64, 5, False),
+                                           (1, 64, 4, True), (B + 1, 64, 4, False), (B, 64, 4, True)):
+        dims.batch, dims.head_dim, dims.q_heads = batch, head_dim, q_heads
+        before = len(calls)
+        if fits:
+            assert qsa.qsa_append_tokens(dims, qsa.QsaInputs(), t, ws, 0) == 0
+        else:
+            with pytest.raises(ValueError):
+                qsa.qsa_append_tokens(dims, qsa.QsaInputs(), t, ws, 0)
+        assert len(calls) == before + fits

@@ -121,6 +121,8 @@ class QsaNewTokens(ctypes.Structure):
     _fields_ = ([(n, QsaProjection) for n in ("q", "k", "v", "q_idx", "idx_key")] +
                 [("type", ctypes.c_int32), ("axes", ctypes.c_int32), ("positions", ctypes.c_void_p),
                  ("turn", QsaRotation), ("turn_idx", QsaRotation), ("eps", ctypes.c_float)])
+    _sizes = None  # of the tensors that `of` was given
+    _fits = None   # the dims that `check` has last found room for (a comparison costs a call 0.1 us, the check 1 us)
 
     @classmethod
     def of(cls, q=None, k=None, v=None, q_idx=None, idx_key=None, *, positions=None, freq=None, idx_freq=None,
@@ -165,16 +167,6 @@ class QsaNewTokens(ctypes.Structure):
         self._sizes = sizes
         self._places = {n: (x.rows, x.norm) for n, x in made.items()}, self.positions
         self._position_row = None if positions is None else int(positions.shape[-1])
-        # what any call may ask for, so that one that asks for less is let through by a few comparisons
-        turned = self._turned()
-        least = lambda values: min((v for v in values if v is not None), default=1 << 62)
-        self._room = (least([r for r, _, _ in sizes.values()] + [self._position_row if turned else None]),
-                      self._position_row if turned and axes > 1 else None,
-                      least([n for k, (_, n, _) in sizes.items() if k == "q"]), least([n for k, (_, n, _) in sizes.items() if k in "kv"]),
-                      least([n for k, (_, n, _) in sizes.items() if k == "q_idx"]),
-                      least([n for k, (_, n, _) in sizes.items() if k == "idx_key"]),
-                      least([n for k, (_, _, n) in sizes.items() if k in "qk"]),
-                      least([n for k, (_, _, n) in sizes.items() if k in ("q_idx", "idx_key")]))
         return self
 
     def _turned(self):
@@ -186,13 +178,9 @@ class QsaNewTokens(ctypes.Structure):
         or positions than the batch has queries (of several axes also more positions, which would be read from the
         wrong places), rows shorter than their heads, norms shorter than a head.  A pointer that was put in the
         place of such a tensor's later is taken as it is."""
-        room = getattr(self, "_room", None)
-        if room is None:
+        if self._sizes is None:
             return
         batch, d, di = dims.batch, dims.head_dim, dims.idx_dim
-        if (batch <= room[0] and (room[1] is None or batch == room[1]) and dims.q_heads * d <= room[2] and
-                dims.kv_heads * d <= room[3] and dims.idx_heads * di <= room[4] and di <= room[5] and d <= room[6] and di <= room[7]):
-            return
         heads = {"q": dims.q_heads, "k": dims.kv_heads, "v": dims.kv_heads, "q_idx": dims.idx_heads, "idx_key": 1}
         places, positions = self._places
         for name, (rows, elements, norm) in self._sizes.items():
@@ -207,6 +195,7 @@ class QsaNewTokens(ctypes.Structure):
         n = self._position_row
         if n is not None and self.positions == positions and self._turned() and (n < batch or (self.axes > 1 and n != batch)):
             raise ValueError(f"positions have {n} entries an axis, the batch {batch} queries")
+        self._fits = bytes(dims)
 
 
 _lib = None
@@ -607,7 +596,8 @@ def qsa_append_tokens(dims, inputs, tokens, ws, stream=None) -> int:
     """Normalises and rotates the new token (the last visible one) of every query and writes it where `inputs`
     points: q, q_idx, its row of idx_keys, its slot of k_cache / v_cache.  Tokens made of tensors that are too
     small for dims raise ValueError."""
-    tokens.check(dims)
+    if tokens._fits != bytes(dims):
+        tokens.check(dims)
     p, n = _ws(ws)
     return _check("qsa_append_tokens", load().qsa_append_tokens(
         ctypes.byref(dims), ctypes.byref(inputs), ctypes.byref(tokens), p, n, _stream(stream)))
